@@ -19,6 +19,10 @@ GQA_ERR_UNSUPPORTED = 2
 GQA_ERR_CUDA = 3
 GQA_ERR_WORKSPACE = 4
 GQA_ERR_TIMEOUT = 5
+GQA_ERR_PAGES = 6
+
+GQA_E4M3 = 0
+GQA_INT8 = 1
 
 _lib = None
 
@@ -50,6 +54,15 @@ _SIGNATURES = {
     "gqa_set_prefill_grid_cap": (None, [_I]),
     "gqa_selftest_exp2_poly": (_I, [_P, _P, _I, _P]),
     "gqa_attn_fwd_rope": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _F, _P]),
+    "gqa_cache8_append": (_I, [_P] * 9 + [_I] * 9 + [_P]),
+    "gqa_cache8_read": (_I, [_P] * 8 + [_I] * 9 + [_P]),
+    "gqa_cache8_copy": (_I, [_P] * 5 + [_I] * 6 + [_P]),
+    "gqa_decode8_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "gqa_decode8": (_I, [_P] * 8 + [_I] * 11 + [_F, _F, _P, ctypes.c_size_t, _P]),
+    "gqa_pages_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
+    "gqa_pages_resize": (_I, [_P] * 3 + [_I] * 4 + [_P, ctypes.c_size_t, _P]),
+    "gqa_pages_fork": (_I, [_P] * 5 + [_I] * 4 + [_P, ctypes.c_size_t, _P]),
+    "gqa_pages_compact": (_I, [_P] * 3 + [_I] * 4 + [_P, ctypes.c_size_t, _P]),
     "gqa_decode_rope": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P, ctypes.c_size_t,
                              _P]),
 }
@@ -152,6 +165,55 @@ def gqa_rope_qk(q, k, B, T, Hq, Hkv, d, pos0, theta, stream):
 
 def gqa_rope_decode_q(q, seqlens, B, H, d, theta, stream):
     return lib().gqa_rope_decode_q(q, seqlens, B, H, d, theta, stream)
+
+
+def gqa_cache8_append(k_cache, v_cache, k_scale, v_scale, table, seqlens, counts, k, v, kind, B, T,
+                      M, n_pages, Hkv, page, d, block, stream):
+    return lib().gqa_cache8_append(k_cache, v_cache, k_scale, v_scale, table, seqlens, counts, k, v,
+                                   kind, B, T, M, n_pages, Hkv, page, d, block, stream)
+
+
+def gqa_cache8_read(k_cache, v_cache, k_scale, v_scale, table, seqlens, k, v, kind, B, T, M, n_pages,
+                    Hkv, page, d, block, stream):
+    return lib().gqa_cache8_read(k_cache, v_cache, k_scale, v_scale, table, seqlens, k, v, kind, B, T,
+                                 M, n_pages, Hkv, page, d, block, stream)
+
+
+def gqa_cache8_copy(k_cache, v_cache, k_scale, v_scale, moves, cap, n_pages, Hkv, page, d, block,
+                    stream):
+    return lib().gqa_cache8_copy(k_cache, v_cache, k_scale, v_scale, moves, cap, n_pages, Hkv, page, d,
+                                 block, stream)
+
+
+def gqa_decode8_workspace_size(B, Hq, Hkv, d, Lmax):
+    return lib().gqa_decode8_workspace_size(B, Hq, Hkv, d, Lmax)
+
+
+def gqa_decode8(q, k_cache, v_cache, k_scale, v_scale, table, seqlens, o, kind, B, Hq, Hkv, d, M,
+                n_pages, page, block, window, sinks, scale, theta, workspace, workspace_bytes, stream):
+    return lib().gqa_decode8(q, k_cache, v_cache, k_scale, v_scale, table, seqlens, o, kind, B, Hq, Hkv,
+                             d, M, n_pages, page, block, window, sinks, scale, theta, workspace,
+                             workspace_bytes, stream)
+
+
+def gqa_pages_workspace_size(B, M, n_pages):
+    return lib().gqa_pages_workspace_size(B, M, n_pages)
+
+
+def gqa_pages_resize(table, refs, lengths, B, M, n_pages, page, workspace, workspace_bytes, stream):
+    return lib().gqa_pages_resize(table, refs, lengths, B, M, n_pages, page, workspace,
+                                  workspace_bytes, stream)
+
+
+def gqa_pages_fork(table, refs, seqlens, parents, moves, B, M, n_pages, page, workspace,
+                   workspace_bytes, stream):
+    return lib().gqa_pages_fork(table, refs, seqlens, parents, moves, B, M, n_pages, page, workspace,
+                                workspace_bytes, stream)
+
+
+def gqa_pages_compact(table, refs, moves, B, M, n_pages, page, workspace, workspace_bytes, stream):
+    return lib().gqa_pages_compact(table, refs, moves, B, M, n_pages, page, workspace,
+                                   workspace_bytes, stream)
 
 
 def gqa_last_error():

@@ -6,7 +6,9 @@ the computation runs in libgqa.so.  Non-OK statuses become exceptions:
 ``NotImplementedError`` for unsupported shapes, ``RuntimeError`` otherwise.
 """
 
+import contextlib
 import math
+from typing import NamedTuple
 
 import torch
 
@@ -273,6 +275,237 @@ def rope_decode_q_(q, seqlens, theta=10000.0):
     _check(_b.gqa_rope_decode_q(q.data_ptr(), seqlens.data_ptr(), B, H, d, float(theta),
                                 _stream(q)), "gqa_rope_decode_q")
     return q
+
+
+# ------------------------------------------------- the paged 8-bit K/V cache --
+
+class Cache8(NamedTuple):
+    """K and V in pages of 8-bit values: k, v [n_pages, Hkv, page, d] (float8_e4m3fn or
+    int8) and the fp32 scales k_scale, v_scale [n_pages, Hkv, page // block] of each
+    block of tokens and head.  A table [B, M] int32 names each sequence's pages."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+_KIND8 = {torch.float8_e4m3fn: _b.GQA_E4M3, torch.int8: _b.GQA_INT8}
+
+
+def cache8(n_pages, Hkv, d, page=64, block=64, dtype=torch.float8_e4m3fn, device=None):
+    """An empty Cache8 of n_pages pages of ``page`` rows, scales per ``block`` rows."""
+    if page < 1 or block < 1 or page % block:
+        raise ValueError(f"block={block} must divide page={page}")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    pool, scale = (n_pages, Hkv, page, d), (n_pages, Hkv, page // block)
+    return Cache8(torch.zeros(pool, dtype=torch.uint8, device=dev).view(dtype),
+                  torch.zeros(pool, dtype=torch.uint8, device=dev).view(dtype),
+                  torch.zeros(scale, dtype=torch.float32, device=dev),
+                  torch.zeros(scale, dtype=torch.float32, device=dev))
+
+
+def _cache8(cache):
+    """Checks a Cache8; returns (kind, n_pages, Hkv, page, d, block)."""
+    k, v, ks, vs = cache
+    kind = _KIND8.get(getattr(k, "dtype", None))
+    if kind is None:
+        raise ValueError(f"the cache must be torch.float8_e4m3fn or torch.int8, got {getattr(k, 'dtype', k)}")
+    _need(k, "cache.k", k.dtype, 4)
+    _need(v, "cache.v", k.dtype, 4)
+    _need(ks, "cache.k_scale", torch.float32, 3)
+    _need(vs, "cache.v_scale", torch.float32, 3)
+    n_pages, Hkv, page, d = k.shape
+    n, h, nblk = ks.shape
+    if v.shape != k.shape or vs.shape != ks.shape or n != n_pages or h != Hkv or nblk < 1 or page % nblk:
+        raise ValueError(f"cache shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}, "
+                         f"k_scale {tuple(ks.shape)}, v_scale {tuple(vs.shape)}")
+    return kind, n_pages, Hkv, page, d, page // nblk
+
+
+def _rows_of(table, *vectors):
+    """Checks a page table and int32 [B] vectors given as (tensor, name); returns (B, M)."""
+    _need(table, "table", torch.int32, 2)
+    B, M = table.shape
+    for t, name in vectors:
+        _need(t, name, torch.int32, 1)
+        if t.shape[0] != B:
+            raise ValueError(f"{name} must have {B} entries, one per table row, got {t.shape[0]}")
+    return B, M
+
+
+def _on(t, *others):
+    """Checks that the tensors share a device; makes it the current one."""
+    dev = t.device
+    for x in others:
+        if x.device != dev:
+            raise ValueError(f"tensors on {dev} and {x.device}: one device is needed")
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _scratch(workspace, need, like):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    return workspace
+
+
+def cache8_append_(cache, table, seqlens, k, v, counts=None):
+    """Quantise new rows into a Cache8, in place: the first counts[b] (default T) rows
+    of bf16 k, v [B, T, Hkv, d] become rows seqlens[b], seqlens[b] + 1, ... of sequence
+    b (table [B, M], seqlens, counts [B] int32; seqlens is not changed).  The scale of a
+    block is the smallest power of two that covers its rows; rows already in a block
+    are requantised when its scale grows.  The page of row seqlens[b] must belong to
+    sequence b alone.  Returns cache."""
+    kind, n_pages, Hkv, page, d, block = _cache8(cache)
+    B, M = _rows_of(table, (seqlens, "seqlens"), *(() if counts is None else ((counts, "counts"),)))
+    _need(k, "k", torch.bfloat16, 4)
+    _need(v, "v", torch.bfloat16, 4)
+    T = k.shape[1]
+    if tuple(k.shape) != (B, T, Hkv, d) or v.shape != k.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [{B}, T, {Hkv}, {d}]")
+    with _on(k, v, table, seqlens, *cache, *(() if counts is None else (counts,))):
+        rc = _b.gqa_cache8_append(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                                  cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(),
+                                  None if counts is None else counts.data_ptr(), k.data_ptr(),
+                                  v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block, _stream(k))
+    _check(rc, "gqa_cache8_append")
+    return cache
+
+
+def cache8_read(cache, table, seqlens, T, out=None):
+    """Rows 0 .. T - 1 of every sequence as bf16 (k, v), each [B, T, Hkv, d] (``out``: that
+    pair of tensors); rows at and past seqlens[b] are zeros."""
+    kind, n_pages, Hkv, page, d, block = _cache8(cache)
+    B, M = _rows_of(table, (seqlens, "seqlens"))
+    T = int(T)
+    if T < 0:
+        raise ValueError(f"T={T} must be >= 0")
+    shape = (B, T, Hkv, d)
+    k, v = out if out is not None else (torch.empty(shape, dtype=torch.bfloat16, device=table.device),
+                                        torch.empty(shape, dtype=torch.bfloat16, device=table.device))
+    for t, n in ((k, "out[0]"), (v, "out[1]")):
+        _need(t, n, torch.bfloat16, 4)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} shape {tuple(t.shape)} != {shape}")
+    with _on(table, seqlens, k, v, *cache):
+        rc = _b.gqa_cache8_read(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                                cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(), k.data_ptr(),
+                                v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block, _stream(table))
+    _check(rc, "gqa_cache8_read")
+    return k, v
+
+
+def cache8_copy_(cache, moves):
+    """Apply page moves (int32 [1 + cap, 3], from pages_fork_ or pages_compact_) to a Cache8,
+    in place: moves[0, 0] moves (src, dst, rows), each replacing the first ``rows`` rows of
+    page dst by those of page src.  A page may be the destination of one move only and
+    then occur in no other.  Returns cache."""
+    _, n_pages, Hkv, page, d, block = _cache8(cache)
+    _need(moves, "moves", torch.int32, 2)
+    if moves.shape[0] < 1 or moves.shape[1] != 3:
+        raise ValueError(f"moves must be [1 + cap, 3], got {tuple(moves.shape)}")
+    with _on(moves, *cache):
+        rc = _b.gqa_cache8_copy(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                                cache[3].data_ptr(), moves.data_ptr(), moves.shape[0] - 1, n_pages, Hkv,
+                                page, d, block, _stream(moves))
+    _check(rc, "gqa_cache8_copy")
+    return cache
+
+
+def decode8_workspace_size(B, Hq, Hkv, d, Lmax):
+    """Bytes of workspace for decode8 on tables of Lmax = M * page rows."""
+    return int(_b.gqa_decode8_workspace_size(B, Hq, Hkv, d, Lmax))
+
+
+def decode8(q, cache, table, seqlens, scale=None, workspace=None, out=None, window=None, sinks=0,
+            rope_theta=None):
+    """One query token per sequence against a Cache8: ``decode`` for a paged 8-bit cache.
+
+    q [B, Hq, d] bf16, table [B, M] and seqlens [B] int32 on the device; returns
+    [B, Hq, d].  ``window`` (an int >= 1) leaves the newest ``window`` rows and the first
+    ``sinks`` visible.  ``rope_theta`` rotates q as it is loaded (position
+    max(seqlens[b] - 1, 0)); the cached keys must already be rotated.  ``workspace``: a
+    uint8 CUDA tensor of at least decode8_workspace_size(...) bytes (allocated here when
+    None)."""
+    kind, n_pages, Hkv, page, d, block = _cache8(cache)
+    B, M = _rows_of(table, (seqlens, "seqlens"))
+    _need(q, "q", torch.bfloat16, 3)
+    Hq = q.shape[1]
+    if tuple(q.shape) != (B, Hq, d):
+        raise ValueError(f"q {tuple(q.shape)} must be [{B}, Hq, {d}]")
+    if window is not None and int(window) < 1:
+        raise ValueError(f"window={window} must be >= 1")
+    if rope_theta is not None and not float(rope_theta) > 0.0:
+        raise ValueError(f"rope_theta={rope_theta} must be > 0")
+    o = torch.empty_like(q) if out is None else out
+    if out is not None:
+        _need(o, "out", torch.bfloat16, 3)
+        if o.shape != q.shape:
+            raise ValueError(f"out shape {tuple(o.shape)} != q shape {tuple(q.shape)}")
+    workspace = _scratch(workspace, _b.gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page), q)
+    with _on(q, o, table, seqlens, workspace, *cache):
+        rc = _b.gqa_decode8(q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                            cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), kind,
+                            B, Hq, Hkv, d, M, n_pages, page, block, 0 if window is None else int(window),
+                            int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+                            0.0 if rope_theta is None else float(rope_theta), workspace.data_ptr(),
+                            workspace.numel(), _stream(q))
+    _check(rc, "gqa_decode8")
+    return o
+
+
+def pages_workspace_size(B, M, n_pages):
+    """Bytes of workspace for the pages_* calls on a table [B, M] and refs [n_pages]."""
+    return int(_b.gqa_pages_workspace_size(B, M, n_pages))
+
+
+def _pages(table, refs, workspace, *vectors):
+    B, M = _rows_of(table, *vectors)
+    _need(refs, "refs", torch.int32, 1)
+    n = refs.shape[0]
+    return B, M, n, _scratch(workspace, _b.gqa_pages_workspace_size(B, M, n), table)
+
+
+def pages_resize_(table, refs, lengths, page, workspace=None):
+    """Give row b of a page table [B, M] exactly the pages that lengths[b] rows need, in
+    place: pages past them are released (refs [n_pages] counts the entries that name a
+    page), missing ones taken from the free pages, lowest first.  lengths[b] = 0 frees
+    the row.  device_status raises if the pool ran out.  Returns table."""
+    B, M, n, ws = _pages(table, refs, workspace, (lengths, "lengths"))
+    with _on(table, refs, lengths, ws):
+        rc = _b.gqa_pages_resize(table.data_ptr(), refs.data_ptr(), lengths.data_ptr(), B, M, n, int(page),
+                                 ws.data_ptr(), ws.numel(), _stream(table))
+    _check(rc, "gqa_pages_resize")
+    return table
+
+
+def pages_fork_(table, refs, seqlens, parents, page, workspace=None):
+    """Row b becomes a copy of the old row parents[b] (int32 [B]; negative: empty), all rows
+    at once and in place, seqlens too: full pages are shared, and every child but one
+    gets a page of its own for the last, partly filled one.  Returns the moves
+    [1 + B, 3] to apply with cache8_copy_ to each cache that uses the table."""
+    B, M, n, ws = _pages(table, refs, workspace, (seqlens, "seqlens"), (parents, "parents"))
+    moves = torch.empty((1 + B, 3), dtype=torch.int32, device=table.device)
+    with _on(table, refs, seqlens, parents, ws):
+        rc = _b.gqa_pages_fork(table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(), parents.data_ptr(),
+                               moves.data_ptr(), B, M, n, int(page), ws.data_ptr(), ws.numel(),
+                               _stream(table))
+    _check(rc, "gqa_pages_fork")
+    return moves
+
+
+def pages_compact_(table, refs, page, workspace=None):
+    """Move the pages in use to the lowest numbers, in place.  Returns the moves
+    [1 + n_pages // 2, 3] to apply with cache8_copy_ to each cache that uses the table."""
+    B, M, n, ws = _pages(table, refs, workspace)
+    moves = torch.empty((1 + n // 2, 3), dtype=torch.int32, device=table.device)
+    with _on(table, refs, ws):
+        rc = _b.gqa_pages_compact(table.data_ptr(), refs.data_ptr(), moves.data_ptr(), B, M, n, int(page),
+                                  ws.data_ptr(), ws.numel(), _stream(table))
+    _check(rc, "gqa_pages_compact")
+    return moves
 
 
 def device_status(reset=True):

@@ -1,0 +1,89 @@
+// cache8.cuh -- the paged 8-bit K/V cache: its geometry and argument checks
+// (host) and the conversions of its 8-bit values (device).
+//
+// K and V lie in pages [n_pages, Hkv, page, d] of 8-bit values, head-major so
+// that the rows of one head in one page are contiguous (page * d bytes): a
+// decode CTA, which reads one head, streams whole lines of DRAM.  The rows of
+// a page fall into blocks of `block` tokens; block b of head h has one fp32
+// scale, [n_pages, Hkv, page / block], and a byte x stands for x * scale.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "device.cuh"
+#include "internal.h"
+
+namespace gqa {
+
+struct Cache8 {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int kind, n_pages, Hkv, page, d, block;
+};
+
+constexpr int kC8Rows = 16;          // page and block are multiples of this
+constexpr int kC8MaxPage = 1024;
+constexpr int kC8MaxBlock = 256;
+
+// Geometry, then (need_ptrs) the pointers; GQA_OK or the error set.
+int check_cache8(const Cache8 &c, bool need_ptrs);
+// B rows of M page slots; M * page must fit an int.
+int check_table(int B, int M, int page);
+
+// Two e4m3 bytes -> two f16 (exact: 4 significant bits, exponents -9 .. 8).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
+    return r;
+}
+
+// The low / high byte pair of a word of four 8-bit values as two f16, exactly.
+// int8: byte x + 128 in the low bits of the f16 1024 is 1152 + x.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t lo_f16x2(uint32_t w) {
+    if constexpr (kInt8) {
+        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, 0x4140);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return e4m3x2_to_f16x2(static_cast<uint16_t>(w));
+}
+
+template <bool kInt8>
+__device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) {
+    if constexpr (kInt8) {
+        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, 0x4342);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+}
+
+// Four 8-bit values -> fp32.
+template <bool kInt8>
+__device__ __forceinline__ void to_f32x4(uint32_t w, float (&f)[4]) {
+    const uint32_t a = lo_f16x2<kInt8>(w), b = hi_f16x2<kInt8>(w);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    f[0] = x.x;
+    f[1] = x.y;
+    f[2] = y.x;
+    f[3] = y.y;
+}
+
+// Four fp32 -> 8-bit values, nearest even.  Beyond the range: the largest value
+// of that sign; NaN stays NaN in e4m3 and becomes 0 in int8.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t from_f32x4(float a, float b, float c, float d) {
+    if constexpr (kInt8) {
+        const int x = max(-127, min(127, __float2int_rn(a))), y = max(-127, min(127, __float2int_rn(b)));
+        const int z = max(-127, min(127, __float2int_rn(c))), w = max(-127, min(127, __float2int_rn(d)));
+        return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+    }
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+}  // namespace gqa

@@ -164,12 +164,28 @@ int encode_tmap_bf16_4d(CUtensorMap *map, const void *base, uint64_t n0, uint64_
     return GQA_OK;
 }
 
+int encode_tmap_rows128(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return set_error(GQA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[2] = {128, rows};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(GQA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llu rows", (int)r,
+                         (unsigned long long)rows);
+    return GQA_OK;
+}
+
 // ------------------------------------------------------------ validation --
 static bool aligned(const void *p, size_t a) {
     return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-static int check_heads(int Hq, int Hkv, int d) {
+int check_heads(int Hq, int Hkv, int d) {
     if (Hq < 1 || Hkv < 1) return set_error(GQA_ERR_INVALID_ARG, "Hq=%d, Hkv=%d must be >= 1", Hq, Hkv);
     if (Hq % Hkv != 0)
         return set_error(GQA_ERR_INVALID_ARG,
@@ -178,16 +194,32 @@ static int check_heads(int Hq, int Hkv, int d) {
     return GQA_OK;
 }
 
-static int check_scale(float scale) {
+int check_scale(float scale) {
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return set_error(GQA_ERR_INVALID_ARG, "scale=%g must be finite and > 0", (double)scale);
     return GQA_OK;
 }
 
-static int check_ptr(const void *p, size_t align, const char *name) {
+int check_ptr(const void *p, size_t align, const char *name) {
     if (!p) return set_error(GQA_ERR_INVALID_ARG, "%s is NULL", name);
     if (!aligned(p, align))
         return set_error(GQA_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
+    return GQA_OK;
+}
+
+int check_theta(float theta) {
+    if (!(theta > 0.0f) || !std::isfinite(theta))
+        return set_error(GQA_ERR_INVALID_ARG, "theta=%g must be finite and > 0", (double)theta);
+    return GQA_OK;
+}
+
+int check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (need == 0) return GQA_OK;
+    if (!workspace) return set_error(GQA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+    if (!aligned(workspace, 256))
+        return set_error(GQA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (bytes < need)
+        return set_error(GQA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", bytes, need);
     return GQA_OK;
 }
 
@@ -235,12 +267,6 @@ static int attn_fwd_bf16(const void *q, const void *k, const void *v, void *o, f
     if (int rc = check_ptr(v, 16, "v")) return rc;
     return launch_prefill(q, k, v, o, lse, B, Tq, Tkv, Hq, Hkv, d, causal, window, sinks, scale,
                           s, 0, 0, rope_theta, q_pos0);
-}
-
-static int check_theta(float theta) {
-    if (!(theta > 0.0f) || !std::isfinite(theta))
-        return set_error(GQA_ERR_INVALID_ARG, "theta=%g must be finite and > 0", (double)theta);
-    return GQA_OK;
 }
 
 int gqa_attn_fwd_host(const void *q_host, const void *k_host, const void *v_host, void *o_host,
@@ -366,14 +392,7 @@ static int decode_bf16(const void *q, const void *k_cache, const void *v_cache,
         return rc;
     if (B == 0) return GQA_OK;
     const size_t need = decode_workspace_bytes(B, Hq, Hkv, d, Lmax);
-    if (need > 0) {
-        if (!workspace) return set_error(GQA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
-        if (!aligned(workspace, 256))
-            return set_error(GQA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-        if (workspace_bytes < need)
-            return set_error(GQA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
-                             workspace_bytes, need);
-    }
+    if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
     if (int rc = require_sm100()) return rc;
     return launch_decode(q, k_cache, v_cache, seqlens, o, B, Hq, Hkv, d, Lmax, window, sinks,
                          scale, workspace, reinterpret_cast<cudaStream_t>(stream), rope_theta);
@@ -436,14 +455,7 @@ int gqa_attn_bwd(const void *q, const void *k, const void *v, const void *o, con
     if (Tq > 0 && !lse) return set_error(GQA_ERR_INVALID_ARG, "lse is NULL");
     if (lse && !aligned(lse, 4)) return set_error(GQA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
     const size_t need = bwd_workspace_bytes(B, Tq, Hq);
-    if (need > 0) {
-        if (!workspace) return set_error(GQA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
-        if (!aligned(workspace, 256))
-            return set_error(GQA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-        if (workspace_bytes < need)
-            return set_error(GQA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed",
-                             workspace_bytes, need);
-    }
+    if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
     if (int rc = require_sm100()) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (Tq == 0) {
@@ -486,6 +498,8 @@ int gqa_device_status(int reset) {
     }
     if (status == GQA_ERR_TIMEOUT)
         return set_error(GQA_ERR_TIMEOUT, "a bounded device wait timed out");
+    if (status == GQA_ERR_PAGES)
+        return set_error(GQA_ERR_PAGES, "a page pool had too few free pages");
     if (status != 0) return set_error(status, "a kernel recorded status %d", status);
     return GQA_OK;
 }

@@ -82,6 +82,22 @@ int encode_tmap_bf16_4d(CUtensorMap *map, const void *base, uint64_t n0, uint64_
                         uint64_t n2, uint64_t n3, uint32_t b0, uint32_t b1, uint32_t b2,
                         uint32_t b3, int swizzle128, uint64_t n2_pitch = 0);
 
+// 2-D map over `rows` consecutive 128-byte rows, box of box_rows whole rows,
+// 128-byte swizzle.  Returns GQA_OK or GQA_ERR_CUDA.
+int encode_tmap_rows128(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
+
+// Argument checks shared by the entry points; each sets the message and
+// returns GQA_OK or GQA_ERR_INVALID_ARG / GQA_ERR_WORKSPACE.
+int check_ptr(const void *p, size_t align, const char *name);
+int check_heads(int Hq, int Hkv, int d);
+int check_scale(float scale);
+int check_theta(float theta);
+int check_workspace(const void *workspace, size_t bytes, size_t need);
+
+// Per-call ids for arrival words in a decode workspace: 48 bits, never 0,
+// different for every launch of the process.
+unsigned long long next_call_id();
+
 // ---- launchers (arguments already validated by the C-ABI layer) ----------
 int launch_fwd_f32(const float *q, const float *k, const float *v, float *o, float *lse,
                    int B, int Tq, int Tkv, int Hq, int Hkv, int d, int causal, float scale,

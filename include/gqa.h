@@ -49,8 +49,15 @@ typedef enum {
     GQA_ERR_UNSUPPORTED = 2,   /* valid but not built: head dim or group size, no sm_100 GPU */
     GQA_ERR_CUDA = 3,          /* a CUDA runtime/driver call failed (launch, tensor map) */
     GQA_ERR_WORKSPACE = 4,     /* decode workspace missing or too small */
-    GQA_ERR_TIMEOUT = 5        /* a bounded device-side wait ran out (see gqa_device_status) */
+    GQA_ERR_TIMEOUT = 5,       /* a bounded device-side wait ran out (see gqa_device_status) */
+    GQA_ERR_PAGES = 6          /* a page pool had too few free pages (see gqa_device_status) */
 } gqa_status;
+
+/* 8-bit types of the paged cache (gqa_cache8_*, gqa_decode8) */
+typedef enum {
+    GQA_E4M3 = 0,              /* float8 e4m3 (finite, +-448) */
+    GQA_INT8 = 1               /* -127 .. 127 */
+} gqa_kind8;
 
 /*
  * gqa_attn_fwd -- prefill / full-sequence forward, bf16 in, bf16 out, fp32
@@ -329,6 +336,144 @@ int gqa_fold_kv(const void *in, void *out, int B, int T, int H, int g, int d,
                 gqa_stream_t stream);
 
 /*
+ * The paged 8-bit K/V cache.
+ *
+ *   k_cache, v_cache [n_pages, Hkv, page, d]  8-bit values (kind: GQA_E4M3 or GQA_INT8)
+ *   k_scale, v_scale [n_pages, Hkv, page / block] fp32
+ *   table            [B, M] int32: the pages of each sequence, slot by slot; -1: none
+ *
+ * Row j of sequence b lies in page table[b][j / page], row j % page; a byte x
+ * stands for x * scale of its block of `block` tokens and its head.  Pages are
+ * head-major: the rows of one head in one page are contiguous.  d in {64, 128}
+ * (else UNSUPPORTED); page a multiple of 16 up to 1024; block a multiple of 16
+ * up to 256 that divides page; n_pages >= 1, M >= 1; n_pages * Hkv * page and
+ * M * page fit an int (else UNSUPPORTED).  Cache pointers 16-byte, the others
+ * 4-byte aligned.  All int32 arrays are DEVICE arrays and are checked by the
+ * kernels: a length outside [0, M * page] (clamped) and a table entry outside
+ * [0, n_pages) where rows are needed (those rows are left out) are flagged in
+ * gqa_device_status as GQA_ERR_INVALID_ARG.  Entries that no row needs are not
+ * read as pages.  Scales are finite, 0 or >= 2^-126.
+ */
+
+/*
+ * gqa_cache8_append -- quantise new K / V rows into the cache.
+ *
+ *   k, v     [B, T, Hkv, d] bf16; the first counts[b] rows of sequence b become
+ *            its rows seqlens[b] .. seqlens[b] + counts[b] - 1 (counts [B] int32
+ *            in [0, T], or NULL: T rows each).  seqlens is not changed.
+ * The scale of each touched (block, head) becomes
+ *   s = max(s_old, smallest power of two with max |x| <= s X),  X = 448 or 127,
+ * over the finite new values of the block (0 when all are 0, never below
+ * 2^-126), where s_old is the present scale if the block has rows before
+ * seqlens[b], else 0.  A new value is stored as the 8-bit value nearest
+ * x * (1 / s), ties to even; older rows of the block are requantised the same
+ * way from byte * s_old when s > s_old.  +-inf becomes the largest value of its
+ * sign; NaN stays NaN in e4m3 and becomes 0 in int8.
+ * Needed pages must be in the table and the page that holds row seqlens[b]
+ * must belong to one sequence only (gqa_pages_fork sees to that).  k and v
+ * 16-byte aligned.  T = 0 or B = 0 launches nothing.
+ */
+int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                      const int32_t *table, const int32_t *seqlens, const int32_t *counts,
+                      const void *k, const void *v, int kind, int B, int T, int M, int n_pages,
+                      int Hkv, int page, int d, int block, gqa_stream_t stream);
+
+/*
+ * gqa_cache8_read -- rows 0 .. T - 1 of every sequence as bf16 k, v [B, T, Hkv, d]
+ * (written; 16-byte aligned), e.g. the prefix a further prompt chunk attends to
+ * with gqa_attn_fwd.  Each value is byte * scale rounded to bf16 (exact for the
+ * scales gqa_cache8_append writes).  Rows at and past seqlens[b] are zeros.
+ */
+int gqa_cache8_read(const void *k_cache, const void *v_cache, const float *k_scale,
+                    const float *v_scale, const int32_t *table, const int32_t *seqlens, void *k,
+                    void *v, int kind, int B, int T, int M, int n_pages, int Hkv, int page, int d,
+                    int block, gqa_stream_t stream);
+
+/*
+ * gqa_cache8_copy -- apply page moves to a cache (to the cache of every layer
+ * that uses the table): the first `rows` rows of each head of page src, and
+ * their scales, replace those of page dst.
+ *   moves [1 + cap, 3] int32 DEVICE array: moves[0] = (number of moves, 0, 0),
+ *   then (src, dst, rows) each, as gqa_pages_fork and gqa_pages_compact write it.
+ * A number of moves outside [0, cap] (clamped) or a move with a page outside
+ * [0, n_pages) or rows outside [0, page] (skipped) is flagged in
+ * gqa_device_status.  The moves run at the same time: no page may be the
+ * destination of a move and occur in another.
+ */
+int gqa_cache8_copy(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                    const int32_t *moves, int cap, int n_pages, int Hkv, int page, int d, int block,
+                    gqa_stream_t stream);
+
+/* Bytes of device scratch gqa_decode8 needs for caches of Lmax = M * page rows a
+ * sequence; 0 for invalid sizes or when none is needed.  Pure host function. */
+size_t gqa_decode8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax);
+
+/*
+ * gqa_decode8 -- gqa_decode over the paged 8-bit cache: one new query token per
+ * sequence, q [B, Hq, d] bf16, o [B, Hq, d] bf16 (written; zeros for a sequence
+ * without visible rows), seqlens [B] rows in the cache.
+ *   window: 0 for none, else only rows j >= seqlens[b] - window and j < sinks
+ *   are visible (pages that hold no visible row are not read and need not
+ *   exist).  theta: 0 for none, else q is rotated as it is loaded, at position
+ *   max(seqlens[b] - 1, 0), with gqa_rope_decode_q's arithmetic (the cached keys
+ *   are rotated before they are appended).
+ * Hq % Hkv == 0, Hq / Hkv <= 32 (else UNSUPPORTED), B and Hkv <= 65535.
+ * workspace: >= gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page) bytes,
+ * 256-byte aligned, contents on entry irrelevant; calls in flight at the same
+ * time (other streams, captured graphs) need workspaces of their own.
+ * K and V are read once; scores, softmax and output sums are fp32.
+ */
+int gqa_decode8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                const float *v_scale, const int32_t *table, const int32_t *seqlens, void *o, int kind,
+                int B, int Hq, int Hkv, int d, int M, int n_pages, int page, int block, int window,
+                int sinks, float scale, float theta, void *workspace, size_t workspace_bytes,
+                gqa_stream_t stream);
+
+/*
+ * Pages.  refs [n_pages] int32 holds how many table entries name each page; a
+ * page with refs <= 0 is free.  The three calls keep table and refs in step, on
+ * the device; pages are taken lowest first, for the entries that need one in
+ * (row, slot) order.  A pool with too few free pages leaves the last entries at
+ * -1 and flags GQA_ERR_PAGES in gqa_device_status; table entries >= n_pages,
+ * lengths outside [0, M * page] (clamped) and counts that would fall below 0
+ * flag GQA_ERR_INVALID_ARG.  One cache per layer can share a table: the calls
+ * return the page moves to apply to each with gqa_cache8_copy.  workspace:
+ * >= gqa_pages_workspace_size(B, M, n_pages) bytes, 256-byte aligned, contents on
+ * entry irrelevant, one for each call in flight.
+ */
+size_t gqa_pages_workspace_size(int B, int M, int n_pages);
+
+/*
+ * gqa_pages_resize -- give row b pages for lengths[b] rows: entries in slots at
+ * and past ceil(lengths[b] / page) are released and become -1, missing entries
+ * below take free pages.  Releases come first, so released pages may be taken
+ * by the same call.  lengths[b] = 0 frees the row.
+ */
+int gqa_pages_resize(int32_t *table, int32_t *refs, const int32_t *lengths, int B, int M, int n_pages,
+                     int page, void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * gqa_pages_fork -- row b becomes a copy of the old row parents[b], all rows at
+ * once: table, refs and seqlens [B] are rewritten.  parents[b] = b keeps the
+ * row, parents[b] < 0 empties it (parents[b] >= B too, flagged INVALID_ARG).
+ * Pages full of rows are shared.  The last, partly filled page (and slots past
+ * it) goes to one child: the parent's own row if it stays, else the lowest
+ * row; every other child gets a page of its own and a move (src, dst, rows)
+ * in moves [1 + B, 3] (written; see gqa_cache8_copy), in row order.
+ */
+int gqa_pages_fork(int32_t *table, int32_t *refs, int32_t *seqlens, const int32_t *parents,
+                   int32_t *moves, int B, int M, int n_pages, int page, void *workspace,
+                   size_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * gqa_pages_compact -- move the n pages in use to pages 0 .. n - 1: the j-th used
+ * page at or past n moves to the j-th free page below n.  table and refs are
+ * rewritten; moves [1 + n_pages / 2, 3] is written for gqa_cache8_copy.
+ */
+int gqa_pages_compact(int32_t *table, int32_t *refs, int32_t *moves, int B, int M, int n_pages,
+                      int page, void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
  * gqa_last_error -- message for the last non-OK status returned on the
  * calling host thread ("" if none).  Valid until the next call on the thread.
  */
@@ -339,7 +484,8 @@ const char *gqa_last_error(void);
  * first error a kernel recorded since the last reset (GQA_OK if none):
  * GQA_ERR_TIMEOUT when a bounded wait inside a kernel ran out (the kernel
  * then stopped early and its output is incomplete), GQA_ERR_INVALID_ARG for a
- * decode length above Lmax.  reset != 0 clears the record.
+ * decode length above Lmax or a bad entry of a page table, GQA_ERR_PAGES for a
+ * page pool that ran out.  reset != 0 clears the record.
  */
 int gqa_device_status(int reset);
 

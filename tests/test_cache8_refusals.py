@@ -1,0 +1,172 @@
+"""The paged 8-bit cache at the C boundary and in the Python wrappers: what is
+refused before any CUDA call (no GPU needed)."""
+
+import pytest
+import torch
+
+import grouped_query_attention_attn_b200 as gqa
+from grouped_query_attention_attn_b200 import _binding as b
+
+FAKE = 0x10000          # an aligned address that is never dereferenced
+BAD, UNS, WS, OK = b.GQA_ERR_INVALID_ARG, b.GQA_ERR_UNSUPPORTED, b.GQA_ERR_WORKSPACE, b.GQA_OK
+
+GEOMETRY = [
+    (dict(kind=2), BAD), (dict(kind=-1), BAD), (dict(Hkv=0), BAD), (dict(n_pages=0), BAD),
+    (dict(page=8), BAD), (dict(page=24), BAD), (dict(page=2048, block=16), BAD), (dict(block=0), BAD),
+    (dict(block=48), BAD), (dict(page=512, block=512), BAD), (dict(d=96), UNS), (dict(d=0), BAD),
+    (dict(n_pages=1 << 24, Hkv=8), UNS), (dict(B=-1), BAD), (dict(M=0), BAD), (dict(M=1 << 26), UNS),
+    (dict(kc=None), BAD), (dict(vc=FAKE + 8), BAD), (dict(ks=FAKE + 2), BAD), (dict(vs=None), BAD),
+    (dict(table=None), BAD), (dict(lens=FAKE + 1), BAD),
+]
+
+
+def args(**kw):
+    a = dict(kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, table=FAKE, lens=FAKE, counts=FAKE, k=FAKE, v=FAKE,
+             kind=0, B=2, T=4, M=4, n_pages=16, Hkv=2, page=64, d=128, block=32, q=FAKE, o=FAKE, Hq=8,
+             window=0, sinks=0, scale=0.1, theta=0.0, ws=FAKE, ws_bytes=1 << 30, refs=FAKE,
+             parents=FAKE, moves=FAKE, cap=3)
+    a.update(kw)
+    return a
+
+
+def append(**kw):
+    a = args(**kw)
+    return b.gqa_cache8_append(*(a[n] for n in "kc vc ks vs table lens counts k v kind B T M n_pages Hkv "
+                                 "page d block".split()), None)
+
+
+def read(**kw):
+    a = args(**kw)
+    return b.gqa_cache8_read(*(a[n] for n in "kc vc ks vs table lens k v kind B T M n_pages Hkv page d "
+                               "block".split()), None)
+
+
+def copy(**kw):
+    a = args(**kw)
+    return b.gqa_cache8_copy(*(a[n] for n in "kc vc ks vs moves cap n_pages Hkv page d block".split()), None)
+
+
+def decode8(**kw):
+    a = args(**kw)
+    return b.gqa_decode8(*(a[n] for n in "q kc vc ks vs table lens o kind B Hq Hkv d M n_pages page block "
+                           "window sinks scale theta ws ws_bytes".split()), None)
+
+
+def resize(**kw):
+    a = args(**kw)
+    return b.gqa_pages_resize(*(a[n] for n in "table refs lens B M n_pages page ws ws_bytes".split()), None)
+
+
+def fork(**kw):
+    a = args(**kw)
+    return b.gqa_pages_fork(*(a[n] for n in "table refs lens parents moves B M n_pages page ws "
+                              "ws_bytes".split()), None)
+
+
+def compact(**kw):
+    a = args(**kw)
+    return b.gqa_pages_compact(*(a[n] for n in "table refs moves B M n_pages page ws ws_bytes".split()), None)
+
+
+@pytest.mark.parametrize("call", [append, read, decode8])
+@pytest.mark.parametrize("kw,code", GEOMETRY)
+def test_geometry(gqa_lib, call, kw, code):
+    assert call(**kw) == code
+    assert b.gqa_last_error() != ""
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(cap=-1), BAD), (dict(moves=None), BAD), (dict(moves=FAKE + 2), BAD), (dict(n_pages=0), BAD),
+    (dict(block=48), BAD), (dict(d=32), UNS), (dict(kc=None), BAD), (dict(cap=0, kc=None), OK)])
+def test_copy(gqa_lib, kw, code):
+    assert copy(**kw) == code
+
+
+@pytest.mark.parametrize("call,kw,code", [
+    (append, dict(T=-1), BAD), (append, dict(T=0x7fffffff), BAD), (append, dict(k=FAKE + 8), BAD),
+    (append, dict(v=None), BAD), (append, dict(counts=FAKE + 2), BAD), (append, dict(B=0, kc=None), OK),
+    (append, dict(T=0, k=None), OK),
+    (read, dict(T=-1), BAD), (read, dict(T=0x7fffffff), BAD), (read, dict(v=FAKE + 4), BAD),
+    (read, dict(B=0, kc=None), OK), (read, dict(T=0, k=None), OK)])
+def test_rows(gqa_lib, call, kw, code):
+    assert call(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Hq=7), BAD), (dict(Hq=0), BAD), (dict(Hq=66), UNS), (dict(scale=0.0), BAD),
+    (dict(scale=float("nan")), BAD), (dict(theta=-1.0), BAD), (dict(theta=float("inf")), BAD),
+    (dict(window=-1), BAD), (dict(sinks=-1), BAD), (dict(q=None), BAD), (dict(o=FAKE + 8), BAD),
+    (dict(B=65536), UNS), (dict(ws=None), WS), (dict(ws=FAKE + 16), WS), (dict(ws_bytes=64), WS),
+    (dict(B=0, q=None, ws=None), OK)])
+def test_decode8(gqa_lib, kw, code):
+    assert decode8(**kw) == code
+
+
+@pytest.mark.parametrize("call", [resize, fork, compact])
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), BAD), (dict(M=0), BAD), (dict(n_pages=0), BAD), (dict(page=0), BAD),
+    (dict(M=1 << 26, page=64), UNS), (dict(table=None), BAD), (dict(refs=FAKE + 2), BAD),
+    (dict(ws=None), WS), (dict(ws=FAKE + 128), WS), (dict(ws_bytes=100), WS)])
+def test_pages(gqa_lib, call, kw, code):
+    assert call(**kw) == code
+
+
+def test_pages_pointers(gqa_lib):
+    assert resize(lens=None) == BAD
+    assert resize(B=0, table=None, lens=None) == OK
+    assert fork(lens=None) == BAD and fork(parents=FAKE + 1) == BAD and fork(moves=None) == BAD
+    assert compact(moves=FAKE + 3) == BAD
+
+
+def test_codes_match_the_header():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gqa.h")).read()
+    for name in ("GQA_ERR_PAGES", "GQA_E4M3", "GQA_INT8"):
+        assert re.search(rf"{name}\s*=\s*{getattr(b, name)}\b", text)
+
+
+def test_workspace_sizes(gqa_lib):
+    size = b.gqa_decode8_workspace_size
+    n = size(64, 32, 8, 128, 8192)
+    assert n > 0 and n % 256 == 0 and size(64, 32, 8, 128, 16384) > n
+    assert size(64, 32, 8, 128, 1) == 0                 # one split: no partial results
+    assert size(64, 32, 3, 128, 8192) == 0 and size(-1, 32, 8, 128, 8192) == 0
+    assert b.gqa_pages_workspace_size(4, 4, 16) % 256 == 0 and b.gqa_pages_workspace_size(4, 0, 16) == 0
+
+
+def split_tiles(n, rows, most):
+    """The kernel's split rule, restated: tiles per split of n tiles."""
+    t = min(max(-(-n * rows // 444), 2), 16)
+    per = max(t, -(-n // most))
+    splits = -(-n // per)
+    return -(-n // splits) if splits else 1
+
+
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (1, 8), (2, 8), (3, 5), (64, 8), (64, 1), (5, 32), (444, 1), (1000, 8)])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 33, 128, 1000, 2048, 16384])
+def test_every_length_fits_its_splits(B, Hkv, tiles):
+    # a table of `tiles` tiles: no sequence needs more splits than the workspace
+    # and grid have, nor more tiles a split than the kernel's arrays (16)
+    rows = B * Hkv
+    most = max(-(-tiles // 16), min(-(-444 // rows), -(-tiles // 2)))
+    need = 2 * Hkv * B * (64 + 1) * 4                   # Hq = 2 Hkv, d = 64
+    got = b.gqa_decode8_workspace_size(B, 2 * Hkv, Hkv, 64, tiles * 64)
+    assert (got == 0) == (most == 1) and got >= most * need * (most > 1)
+    for n in {*range(1, min(tiles, 300) + 1), *range(max(1, tiles - 50), tiles + 1)}:
+        per = split_tiles(n, rows, most)
+        assert 1 <= per <= 16 and -(-n // per) <= most
+
+
+def test_wrappers_refuse_host_tensors():
+    t = torch.zeros((2, 3), dtype=torch.int32)
+    c = gqa.cache8(4, 2, 64, page=16, block=16, device="cpu")
+    assert c.k.shape == (4, 2, 16, 64) and c.k_scale.shape == (4, 2, 1) and c.k.dtype == torch.float8_e4m3fn
+    with pytest.raises(ValueError):
+        gqa.decode8(torch.zeros((2, 4, 64), dtype=torch.bfloat16), c, t, t[:, 0])
+    with pytest.raises(ValueError):
+        gqa.cache8_read(c, t, t[:, 0].contiguous(), 4)
+    with pytest.raises(ValueError):
+        gqa.pages_resize_(t, t[:, 0].contiguous(), t[:, 0].contiguous(), 16)
+    with pytest.raises(ValueError):
+        gqa.cache8(4, 2, 64, page=16, block=48)
