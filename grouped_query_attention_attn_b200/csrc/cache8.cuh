@@ -30,39 +30,31 @@ int check_cache8(const Cache8 &c, bool need_ptrs);
 // B rows of M page slots; M * page must fit an int.
 int check_table(int B, int M, int page);
 
-// Two e4m3 bytes -> two f16 (exact: 4 significant bits, exponents -9 .. 8).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t w) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
-    return r;
-}
-
-// The low / high byte pair of a word of four 8-bit values as two f16, exactly.
-// int8: byte x + 128 in the low bits of the f16 1024 is 1152 + x.
+// The low and high byte pairs of a word of four 8-bit values as two f16 each,
+// exactly.  e4m3 has 4 significant bits and exponents -9 .. 8; int8: byte x + 128
+// in the low bits of the f16 1024 is 1152 + x.
 template <bool kInt8>
-__device__ __forceinline__ uint32_t lo_f16x2(uint32_t w) {
+__device__ __forceinline__ void to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if constexpr (kInt8) {
-        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, 0x4140);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
-        return *reinterpret_cast<const uint32_t *>(&h);
+        const uint32_t x = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+        const __half2 bias = __float2half2_rn(1152.0f);
+        const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
     }
-    return e4m3x2_to_f16x2(static_cast<uint16_t>(w));
-}
-
-template <bool kInt8>
-__device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) {
-    if constexpr (kInt8) {
-        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, 0x4342);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
 }
 
 // Four 8-bit values -> fp32.
 template <bool kInt8>
 __device__ __forceinline__ void to_f32x4(uint32_t w, float (&f)[4]) {
-    const uint32_t a = lo_f16x2<kInt8>(w), b = hi_f16x2<kInt8>(w);
+    uint32_t a, b;
+    to_f16x2<kInt8>(w, a, b);
     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
     f[0] = x.x;

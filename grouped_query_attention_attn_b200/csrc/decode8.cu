@@ -3,21 +3,28 @@
 //   s_j = scale <q, k_j>,  o = sum_j softmax(s)_j v_j,  k_j, v_j = byte * scale of its block
 //
 // HBM-bound: the cache is read once, 2 d bytes per key and K/V head, and the
-// grid has to keep that stream going.  One CTA per (split, K/V head, sequence):
-//   - warp 4 reads the split's page numbers and issues one TMA box per page
-//     piece (64, 32 or 16 keys, whatever divides the page) into a ring of
-//     64-key stages of K and V, 128-byte swizzle;
-//   - warps 0-3 take 16 keys of every stage.  The G = Hq / Hkv query heads of
-//     the group are the M rows of m16n8k16 f16 products.  e4m3 and int8 values
-//     are exact in f16, so K and V need no scaling to enter the product; q (8
-//     significant bits) is multiplied by a power of two per row to sit at 1 and
-//     is exact in f16 down to 2^-14 of the row's largest value, and absolutely
-//     to 2^-25 of it below.  The 16 keys of a step lie in one scale block: the
-//     K scale multiplies the scores, the V scale the weights (see below).
+// grid has to keep that stream going.  One CTA per (split, K/V head, sequence);
+// its four warps take 32-key tiles in turn, each with a TMA ring of its own: one
+// lane issues a box per page piece (32 or 16 keys, whatever divides the page),
+// 128-byte swizzle, and no warp waits for another before the end of the split.
+// A lane holds the page and the scales of one 16-key group of its warp's tiles.
+//
+// Arithmetic per byte is what competes with the stream, so the products are laid
+// out for few instructions:
+//   - S^T = K Q^T and O^T = V^T P^T as m16n8k16 f16 products with the keys (or
+//     the elements of V) as the M rows and the G = Hq / Hkv query heads of the
+//     group as the N columns, 8 at a time: with the heads as M rows, three
+//     quarters of each product, softmax and rescaling would be padding for G = 4.
+//   - e4m3 and int8 values are exact in f16, so K and V need no scaling to enter
+//     a product; q (8 significant bits) is multiplied by a power of two per row
+//     to sit at 1 and is exact in f16 down to 2^-14 of the row's largest value,
+//     and absolutely to 2^-25 of it below.  The 16 keys of a group lie in one
+//     scale block: the K scale multiplies the scores, the V scale the weights.
 //   - both operands come straight from shared memory as 16-byte loads: the
 //     contraction index of Q K^T may be permuted, so a thread's K fragments are
 //     the 32 consecutive bytes (d = 128) it loads; V's four keys per thread are
-//     paired by byte permutes before the conversion.
+//     paired by byte permutes before the conversion.  P^T is S^T transposed by
+//     movmatrix, 8 x 8 f16 at a time.
 // The running maximum, sums and O stay in fp32; the weights enter the second
 // product in f16 (11 significant bits, at most 2^-12 off).
 //
@@ -36,12 +43,14 @@
 
 namespace gqa {
 
-constexpr int kD8Keys = 64;                        // keys per stage (a tile)
-constexpr int kD8Warps = 4;                        // consumer warps, 16 keys each per stage
-constexpr int kD8Threads = (kD8Warps + 1) * 32;    // + the producer
-constexpr int kD8MaxTiles = 16;                    // tiles per split at most
-constexpr int kD8MinTiles = 2;
+constexpr int kD8Keys = 32;                        // keys per tile
+constexpr int kD8Warps = 4;                        // each takes every fourth tile
+constexpr int kD8Threads = kD8Warps * 32;
+constexpr int kD8Stages = 2;                       // TMA ring of each warp, in tiles
+constexpr int kD8MaxTiles = 32;                    // tiles per split at most
+constexpr int kD8MinTiles = 4;
 constexpr int kD8Ctas = 444;                       // 148 SMs x 3 resident CTAs
+static_assert(kD8MaxTiles / kD8Warps * 2 <= 32, "a lane per 16-key group of a warp");
 
 struct D8Params {
     const __nv_bfloat16 *q;
@@ -57,22 +66,23 @@ struct D8Params {
     int *status;
 };
 
-template <int D, int MB>
+template <int D, int NT>
 struct D8Layout {
-    static constexpr int kTileBytes = kD8Keys * D;          // K or V of one stage
+    static constexpr int kTileBytes = kD8Keys * D;          // K or V of one tile
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kStages = 512 / D;                 // a ring of 64 KB
-    static constexpr int kRingBytes = kStages * kStageBytes;
-    // the end-of-split merge reuses the ring: per warp 16 MB rows of O (four
-    // floats of padding per D / 4, against bank conflicts), m and l
-    static constexpr int kRows = 16 * MB;
-    static constexpr int kRowFloats = D + 16;
+    static constexpr int kRingBytes = kD8Stages * kStageBytes;   // of one warp
+    // the end-of-split merge reuses the rings: per warp 8 NT rows of O, m and l.
+    // Four floats of padding after every D / 8 and at the end of a row spread
+    // the 16-byte stores of a quarter warp over all banks.
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kRowFloats = D + 32 + 4;
     static constexpr int kMergeBytes = kD8Warps * kRows * (kRowFloats + 2) * 4;
-    static constexpr int kBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kBytes =
+        kD8Warps * kRingBytes > kMergeBytes ? kD8Warps * kRingBytes : kMergeBytes;
     static constexpr int kSmemBytes = kBytes + 1024;        // + alignment slack
 };
 
-// Tiles (64 keys) a sequence of L keys reads, in order: those of the sinks
+// Tiles a sequence of L keys reads, in order: those of the sinks
 // below the window, then those from the window's first key on.
 struct D8Tiles {
     int lo, sinks;              // key j is visible iff j < L and (j >= lo or j < sinks)
@@ -122,18 +132,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int D, int MB, bool kInt8, bool kRope>
-__global__ void __launch_bounds__(kD8Threads, MB == 1 ? 3 : 1)
+// Transpose of an 8 x 8 matrix of f16 held one pair per lane.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// NT: tiles of 8 query heads.  kRope: the query is rotated as it is loaded.
+template <int D, int NT, bool kInt8, bool kRope>
+__global__ void __launch_bounds__(kD8Threads, NT == 1 ? 3 : (NT == 2 ? 2 : 1))
 decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const D8Params p) {
-    using Lay = D8Layout<D, MB>;
+    using Lay = D8Layout<D, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    constexpr int kStages = Lay::kStages;
-    __shared__ uint64_t full_bar[kStages], empty_bar[kStages];
-    __shared__ float2 s_scale[kD8MaxTiles * 4];     // (K, V) scale of each 16-key step; V < 0: skip
-    __shared__ int s_page[kD8MaxTiles * 4];         // page of each TMA box, -1: not read
+    __shared__ uint64_t full_bar[kD8Warps][kD8Stages];
     __shared__ int abort_flag, merger;
 
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
@@ -156,359 +171,357 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 reinterpret_cast<uint4 *>(p.o + grow0 * D)[idx] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    const int i0 = split * per;                                  // first tile of the split
-    const int n_iter = min(per, seq.n - i0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t *row = p.table + static_cast<size_t>(b) * p.M;
+    const int i0 = split * per + warp;                           // this warp's first tile
+    const int n_iter = (min(per, seq.n - split * per) - warp + kD8Warps - 1) / kD8Warps;
     auto seen = [&](int key0, int n) {                           // any of n keys visible
         return key0 < L && (key0 + n > seq.lo || key0 < seq.sinks);
     };
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full_bar[s], 1);
-            mbar_init(&empty_bar[s], kD8Warps);
-        }
-        abort_flag = 0;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0) {
+        for (int s = 0; s < kD8Stages; ++s) mbar_init(&full_bar[warp][s], 1);
         fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    // lane i: page of the 16 keys that are half i & 1 of this warp's tile i >> 1
+    int g_page = -1;
+    float g_ks = 0.0f, g_vs = -1.0f;                             // V scale -1: not there
+    const int g_key = seq.tile(i0 + (lane >> 1) * kD8Warps) * kD8Keys + (lane & 1) * 16;
+    if ((lane >> 1) < n_iter && seen(g_key, 16)) {               // g_key < L: the slot exists
+        g_page = p.table[static_cast<size_t>(b) * p.M + g_key / p.page];
+        if (g_page < 0 || g_page >= p.n_pages) {
+            record_status(p.status, GQA_ERR_INVALID_ARG);
+            g_page = -1;
+        }
     }
     __syncthreads();
 
-    if (warp == kD8Warps) {                          // ---- TMA producer ----
-        const int n_box = kD8Keys / p.box;           // boxes per stage
-        for (int i = lane; i < n_iter * n_box; i += 32) {
-            const int key0 = seq.tile(i0 + i / n_box) * kD8Keys + (i % n_box) * p.box;
-            int page = -1;
-            if (seen(key0, p.box)) {                 // key0 < L <= M * page: the slot exists
-                page = row[key0 / p.page];
-                if (page < 0 || page >= p.n_pages) {
-                    record_status(p.status, GQA_ERR_INVALID_ARG);
-                    page = -1;
+    uint8_t *ring = smem + warp * Lay::kRingBytes;
+    // Copies of tile t into its ring slot, counted on the slot's barrier.
+    auto issue = [&](int t) {
+        const int p0 = __shfl_sync(0xffffffffu, g_page, 2 * t);
+        const int p1 = __shfl_sync(0xffffffffu, g_page, 2 * t + 1);
+        if (lane == 0) {
+            uint64_t *bar = &full_bar[warp][t % kD8Stages];
+            uint8_t *kt = ring + (t % kD8Stages) * Lay::kStageBytes;
+            uint8_t *vt = kt + Lay::kTileBytes;
+            const int key0 = seq.tile(i0 + t * kD8Warps) * kD8Keys;
+            // 128-byte row of a key; fits an int (checked on the host)
+            auto row = [&](int page, int key) {
+                return ((page * p.Hkv + kvh) * p.page + key % p.page) / (128 / D);
+            };
+            if (p.box == kD8Keys) {                              // both halves in one page
+                const int page = max(p0, p1);
+                mbar_expect_tx(bar, page >= 0 ? Lay::kStageBytes : 0);
+                if (page >= 0) {
+                    tma_load_2d(kt, &tm_k, bar, 0, row(page, key0));
+                    tma_load_2d(vt, &tm_v, bar, 0, row(page, key0));
+                }
+            } else {
+                mbar_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * (Lay::kStageBytes / 2));
+                if (p0 >= 0) {
+                    tma_load_2d(kt, &tm_k, bar, 0, row(p0, key0));
+                    tma_load_2d(vt, &tm_v, bar, 0, row(p0, key0));
+                }
+                if (p1 >= 0) {
+                    tma_load_2d(kt + Lay::kTileBytes / 2, &tm_k, bar, 0, row(p1, key0 + 16));
+                    tma_load_2d(vt + Lay::kTileBytes / 2, &tm_v, bar, 0, row(p1, key0 + 16));
                 }
             }
-            s_page[i] = page;
         }
         __syncwarp();
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
-            const uint32_t box_bytes = p.box * D;
-            int t = 0;
-            for (; t < n_iter; ++t) {
-                const int st = t % kStages;
-                if (!mbar_wait(&empty_bar[st], ((t / kStages) & 1) ^ 1, &abort_flag, p.status))
-                    break;
-                uint8_t *kt = smem + st * Lay::kStageBytes;
-                uint8_t *vt = kt + Lay::kTileBytes;
-                uint32_t bytes = 0;
-                for (int x = 0; x < n_box; ++x)
-                    if (s_page[t * n_box + x] >= 0) bytes += 2 * box_bytes;
-                mbar_expect_tx(&full_bar[st], bytes);
-                const int key0 = seq.tile(i0 + t) * kD8Keys;
-                for (int x = 0; x < n_box; ++x) {
-                    const int page = s_page[t * n_box + x];
-                    if (page < 0) continue;
-                    // 128-byte row of the box's first key; fits an int (checked on the host)
-                    const int off = (key0 + x * p.box) % p.page;
-                    const int r = ((page * p.Hkv + kvh) * p.page + off) / (128 / D);
-                    tma_load_2d(kt + x * box_bytes, &tm_k, &full_bar[st], 0, r);
-                    tma_load_2d(vt + x * box_bytes, &tm_v, &full_bar[st], 0, r);
-                }
-            }
-            // an aborted split lets its copies land before the block exits
-            if (t < n_iter)
-                for (int u = max(0, t - kStages); u < t; ++u)
-                    mbar_wait(&full_bar[u % kStages], (u / kStages) & 1, &abort_flag, p.status,
-                              1000000ull);
-        }
-        return;                                     // consumers sync with named barrier 1 only
+    };
+    int issued = 0;
+    for (; issued < min(n_iter, kD8Stages); ++issued) issue(issued);
+    if (g_page >= 0) {
+        const size_t at = (static_cast<size_t>(g_page) * p.Hkv + kvh) * p.nblk + g_key % p.page / p.block;
+        g_ks = p.k_scale[at];
+        g_vs = p.v_scale[at];
     }
 
-    // ---- consumers ----
-    for (int i = threadIdx.x; i < n_iter * 4; i += kD8Warps * 32) {
-        const int key0 = seq.tile(i0 + (i >> 2)) * kD8Keys + (i & 3) * 16;
-        float2 sc = make_float2(0.0f, -1.0f);
-        if (seen(key0, 16)) {
-            const int page = row[key0 / p.page];
-            if (page >= 0 && page < p.n_pages) {
-                const size_t at = (static_cast<size_t>(page) * p.Hkv + kvh) * p.nblk +
-                                  key0 % p.page / p.block;
-                sc = make_float2(p.k_scale[at], p.v_scale[at]);
-            }
-        }
-        s_scale[i] = sc;
-    }
-    const int gq = lane >> 2, tq = lane & 3;        // quad row, lane in quad
-    // Query fragments.  Contraction step s multiplies elements 4 s .. 4 s + 3 of
-    // each thread's quarter of the row (D / 4 consecutive elements).
+    const int gq = lane >> 2, tq = lane & 3;        // quad, lane in quad
+    // Query fragments (column gq of head tile nt).  Contraction step s multiplies
+    // elements 4 s .. 4 s + 3 of each thread's quarter of the row (D / 4 elements).
     constexpr int kQ = D / 4;
     const __nv_bfloat16 *qg = p.q + grow0 * D + tq * kQ;
-    uint32_t qa[MB][D / 16][4];
-    float qs[MB][2];                                // scale of the scores of rows gq, gq + 8
+    uint32_t qb[NT][D / 16][2];
+    float qs[NT][2];                                // score scale of heads 2 tq, 2 tq + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + gq;
+#pragma unroll
+        for (int s = 0; s < D / 16; s += 2) {
+            const uint4 w = r < G ? *reinterpret_cast<const uint4 *>(qg + r * D + 4 * s)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+            qb[nt][s][0] = w.x;
+            qb[nt][s][1] = w.y;
+            qb[nt][s + 1][0] = w.z;
+            qb[nt][s + 1][1] = w.w;
+        }
+    }
     if constexpr (kRope) {
         __shared__ float2 rope_cs[D / 2];
         const int m = max(len - 1, 0);
-        for (int i = threadIdx.x; i < D / 2; i += kD8Warps * 32) {
+        for (int i = threadIdx.x; i < D / 2; i += kD8Threads) {
             float cs, sn;
             rope_cos_sin(m, rope_turns(i, D / 2, p.log_theta), cs, sn);
             rope_cs[i] = make_float2(cs, sn);
         }
-        named_barrier_sync(1, kD8Warps * 32);
+        __syncthreads();
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int s = 0; s < D / 16; ++s) {
+            const float2 c0 = rope_cs[tq * (kQ / 2) + 2 * s], c1 = rope_cs[tq * (kQ / 2) + 2 * s + 1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = mb * 16 + h * 8 + gq;
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    uint2 w = r < G ? *reinterpret_cast<const uint2 *>(qg + r * D + 4 * s)
-                                    : make_uint2(0u, 0u);
-                    const float2 c0 = rope_cs[tq * (kQ / 2) + 2 * s], c1 = rope_cs[tq * (kQ / 2) + 2 * s + 1];
-                    qa[mb][s][h] = rope_rotate_pair(w.x, c0.x, c0.y);
-                    qa[mb][s][h + 2] = rope_rotate_pair(w.y, c1.x, c1.y);
-                }
-            }
-    } else {
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = mb * 16 + h * 8 + gq;
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint2 w = r < G ? *reinterpret_cast<const uint2 *>(qg + r * D + 4 * s)
-                                          : make_uint2(0u, 0u);
-                    qa[mb][s][h] = w.x;
-                    qa[mb][s][h + 2] = w.y;
-                }
-            }
-        named_barrier_sync(1, kD8Warps * 32);       // s_scale is complete
-    }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // bring the row's largest value into [1, 2); an infinite or zero row stays as it is
-            float mx = 0.0f;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const float2 a = bf16x2_to_float2(qa[mb][s][h]), c = bf16x2_to_float2(qa[mb][s][h + 2]);
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(c.x), fabsf(c.y))));
-            }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const int e = static_cast<int>(__float_as_uint(mx) >> 23);      // biased exponent
-            const bool fit = e > 0 && e < 255;
-            const uint32_t ex = min(e, 253);        // 2^(ex - 127) and its inverse are normal
-            const float up = fit ? __uint_as_float((254 - ex) << 23) : 1.0f;
-            qs[mb][h] = (fit ? __uint_as_float(ex << 23) : 1.0f) * p.scale_log2;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const float2 a = bf16x2_to_float2(qa[mb][s][h]), c = bf16x2_to_float2(qa[mb][s][h + 2]);
-                qa[mb][s][h] = pack_f16x2(a.x * up, a.y * up);
-                qa[mb][s][h + 2] = pack_f16x2(c.x * up, c.y * up);
+            for (int nt = 0; nt < NT; ++nt) {
+                qb[nt][s][0] = rope_rotate_pair(qb[nt][s][0], c0.x, c0.y);
+                qb[nt][s][1] = rope_rotate_pair(qb[nt][s][1], c1.x, c1.y);
             }
         }
-    float oacc[MB][D / 8][4];
-    float m_run[MB][2], l_run[MB][2];
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        // bring the row's largest value into [1, 2); an infinite or zero row stays as it is
+        float mx = 0.0f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            const float2 a = bf16x2_to_float2(qb[nt][s][0]), c = bf16x2_to_float2(qb[nt][s][1]);
+            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(c.x), fabsf(c.y))));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = static_cast<int>(__float_as_uint(mx) >> 23);          // biased exponent
+        const bool fit = e > 0 && e < 255;
+        const uint32_t ex = min(e, 253);            // 2^(ex - 127) and its inverse are normal
+        const float up = fit ? __uint_as_float((254 - ex) << 23) : 1.0f;
+        const float down = (fit ? __uint_as_float(ex << 23) : 1.0f) * p.scale_log2;
+        qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * tq);
+        qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * tq + 4);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 a = bf16x2_to_float2(qb[nt][s][h]);
+                qb[nt][s][h] = pack_f16x2(a.x * up, a.y * up);
+            }
+    }
+    // O^T: product j, accumulator e is element (D / 8) gq + 2 j + (e >> 1) of head 2 tq + (e & 1)
+    float oacc[NT][D / 16][4];
+    float m_run[NT][2], l_run[NT][2];
     float vref = 0.0f, vinv = 0.0f;                 // O is in units of vref (0: O is still 0)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) oacc[mb][j][e] = 0.0f;
-        m_run[mb][0] = m_run[mb][1] = -INFINITY;
-        l_run[mb][0] = l_run[mb][1] = 0.0f;
+            for (int e = 0; e < 4; ++e) oacc[nt][j][e] = 0.0f;
+        m_run[nt][0] = m_run[nt][1] = -INFINITY;
+        l_run[nt][0] = l_run[nt][1] = 0.0f;
     }
 
     for (int t = 0; t < n_iter; ++t) {
-        const int st = t % kStages;
+        const int st = t % kD8Stages;
         // warp-uniform outcome: the products below are warp-collective
-        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[st], (t / kStages) & 1, &abort_flag,
+        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[warp][st], (t / kD8Stages) & 1, &abort_flag,
                                                p.status)))
             break;
-        const uint8_t *kt = smem + st * Lay::kStageBytes;
+        const uint8_t *kt = ring + st * Lay::kStageBytes;
         const uint8_t *vt = kt + Lay::kTileBytes;
-        const int key0 = seq.tile(i0 + t) * kD8Keys + warp * 16;
-        const float2 sc = s_scale[t * 4 + warp];
-        if (seen(key0, 16) && sc.y != -1.0f) {
-            const bool all = key0 + 16 <= L && (key0 >= seq.lo || key0 + 16 <= seq.sinks);
-            auto visible = [&](int nb, int n) {
-                const int key = key0 + d8_key<D>(nb, n);
-                return key < L && (key >= seq.lo || key < seq.sinks);
-            };
-            // ---- S = Q K^T ----
-            float sacc[MB][2][4];
+        const int key0 = seq.tile(i0 + t * kD8Warps) * kD8Keys;
+        float ks[2], vs[2];
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
+        for (int x = 0; x < 2; ++x) {
+            ks[x] = __shfl_sync(0xffffffffu, g_ks, 2 * t + x);
+            vs[x] = __shfl_sync(0xffffffffu, g_vs, 2 * t + x);
+        }
+        const bool all = key0 + kD8Keys <= L && (key0 >= seq.lo || key0 + kD8Keys <= seq.sinks) &&
+                         vs[0] != -1.0f && vs[1] != -1.0f;
+        auto visible = [&](int x, int nb, int n) {
+            const int key = key0 + x * 16 + d8_key<D>(nb, n);
+            return vs[x] != -1.0f && key < L && (key >= seq.lo || key < seq.sinks);
+        };
+        // ---- S^T = K Q^T: half x, accumulator e is key (e >> 1, gq), head 2 tq + (e & 1) ----
+        float sacc[NT][2][4];
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sacc[mb][nb][e] = 0.0f;
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-                const int key = warp * 16 + d8_key<D>(nb, gq);
+                for (int e = 0; e < 4; ++e) sacc[nt][x][e] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint4 kw = *reinterpret_cast<const uint4 *>(
-                        kt + d8_off<D>(key, tq * (D / 64) + c));
-                    const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t b0 = lo_f16x2<kInt8>(w[x]), b1 = hi_f16x2<kInt8>(w[x]);
+            for (int c = 0; c < D / 64; ++c) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(
+                    kt + d8_off<D>(x * 16 + d8_key<D>(0, gq), tq * (D / 64) + c));
+                const uint4 v = *reinterpret_cast<const uint4 *>(
+                    kt + d8_off<D>(x * 16 + d8_key<D>(1, gq), tq * (D / 64) + c));
+                const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int mb = 0; mb < MB; ++mb)
-                            mma_16816_f16(sacc[mb][nb], qa[mb][c * 4 + x], b0, b1);
-                    }
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t a[4];
+                    to_f16x2<kInt8>(uw[s], a[0], a[2]);
+                    to_f16x2<kInt8>(vw[s], a[1], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816_f16(sacc[nt][x], a, qb[nt][c * 4 + s][0], qb[nt][c * 4 + s][1]);
                 }
             }
-            // ---- V scale of the step: weight factor, and O's change of units ----
-            float pscale = 1.0f, ratio = 1.0f;
-            if (sc.y == 0.0f) {
-                pscale = 0.0f;
-            } else if (sc.y != vref) {
-                if (!(sc.y <= vref && sc.y * 64.0f >= vref)) {
-                    const float nv = fmaxf(sc.y, vref * 5.42101086e-20f);       // 2^-64
-                    if (vref > 0.0f) ratio = vref / nv;
-                    vref = nv;
-                    vinv = nv > 0.0f ? 1.0f / nv : 0.0f;
-                }
-                pscale = sc.y * vinv;
+        // ---- V scales: weight factor of each half, and O's change of units before it ----
+        float pscale[2], ratio[2] = {1.0f, 1.0f};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (vs[x] == 0.0f || vs[x] == -1.0f) {
+                pscale[x] = 0.0f;
+                continue;
             }
-            // ---- softmax step ----
-            uint32_t pa[MB][4];
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                const float f[2] = {qs[mb][0] * sc.x, qs[mb][1] * sc.x};
-                float s[2][4], mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[nb][e] = sacc[mb][nb][e] * f[e >> 1];
-                        if (!all && !visible(nb, 2 * tq + (e & 1))) s[nb][e] = -INFINITY;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], s[nb][e]);
-                    }
-                float alpha[2], m_use[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                    const float m_new = fmaxf(m_run[mb][h], mx[h]);
-                    m_use[h] = (m_new == -INFINITY) ? 0.0f : m_new;
-                    alpha[h] = fast_exp2(m_run[mb][h] - m_use[h]);
-                    m_run[mb][h] = m_new;
-                }
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nb][e] = fast_exp2(s[nb][e] - m_use[e >> 1]);
-                l_run[mb][0] = l_run[mb][0] * alpha[0] + ((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]));
-                l_run[mb][1] = l_run[mb][1] * alpha[1] + ((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]));
-                pa[mb][0] = pack_f16x2(s[0][0] * pscale, s[0][1] * pscale);   // row gq
-                pa[mb][1] = pack_f16x2(s[0][2] * pscale, s[0][3] * pscale);   // row gq + 8
-                pa[mb][2] = pack_f16x2(s[1][0] * pscale, s[1][1] * pscale);
-                pa[mb][3] = pack_f16x2(s[1][2] * pscale, s[1][3] * pscale);
-                // most steps move neither a maximum nor the V reference
-                alpha[0] *= ratio;
-                alpha[1] *= ratio;
-                if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        oacc[mb][j][0] *= alpha[0];
-                        oacc[mb][j][1] *= alpha[0];
-                        oacc[mb][j][2] *= alpha[1];
-                        oacc[mb][j][3] *= alpha[1];
-                    }
-                }
+            if (!(vs[x] <= vref && vs[x] * 64.0f >= vref)) {
+                const float nv = fmaxf(vs[x], vref * 5.42101086e-20f);      // 2^-64
+                if (vref > 0.0f) ratio[x] = vref / nv;
+                vref = nv;
+                vinv = 1.0f / nv;
             }
-            // ---- O += P V: column n of product j is element (D / 8) n + j ----
+            pscale[x] = vs[x] * vinv;
+        }
+        // ---- softmax step ----
+        uint32_t pb[NT][2][2];
+        float alpha[NT][2];
+        bool moved = ratio[0] != 1.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float s[2][4], mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[x][e] = sacc[nt][x][e] * (qs[nt][e & 1] * ks[x]);
+                    if (!all && !visible(x, e >> 1, gq)) s[x][e] = -INFINITY;
+                    mx[e & 1] = fmaxf(mx[e & 1], s[x][e]);
+                }
+            float m_use[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 4));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 8));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
+                const float m_new = fmaxf(m_run[nt][h], mx[h]);
+                m_use[h] = (m_new == -INFINITY) ? 0.0f : m_new;
+                alpha[nt][h] = fast_exp2(m_run[nt][h] - m_use[h]);
+                moved |= alpha[nt][h] != 1.0f;
+                m_run[nt][h] = m_new;
+                l_run[nt][h] *= alpha[nt][h];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[x][e] = fast_exp2(s[x][e] - m_use[e & 1]);
+                l_run[nt][0] += s[x][0] + s[x][2];
+                l_run[nt][1] += s[x][1] + s[x][3];
+                pb[nt][x][0] = transpose_8x8(pack_f16x2(s[x][0] * pscale[x], s[x][1] * pscale[x]));
+                pb[nt][x][1] = transpose_8x8(pack_f16x2(s[x][2] * pscale[x], s[x][3] * pscale[x]));
+            }
+        }
+        // most tiles move neither a maximum nor the V reference
+        auto rescale = [&](int nt, float f0, float f1) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                oacc[nt][j][0] *= f0;
+                oacc[nt][j][1] *= f1;
+                oacc[nt][j][2] *= f0;
+                oacc[nt][j][3] *= f1;
+            }
+        };
+        if (__any_sync(0xffffffffu, moved))
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) rescale(nt, alpha[nt][0] * ratio[0], alpha[nt][1] * ratio[0]);
+        // ---- O^T += V^T P^T ----
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (x == 1 && ratio[1] != 1.0f)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) rescale(nt, ratio[1], ratio[1]);
             constexpr int kW = D / 32;              // words of V per key and thread
             uint32_t vw[4][kW];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int key = warp * 16 + d8_key<D>(x >> 1, 2 * tq + (x & 1));
+            for (int k = 0; k < 4; ++k) {
+                const int key = x * 16 + d8_key<D>(k >> 1, 2 * tq + (k & 1));
                 if constexpr (D == 128) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(vt + d8_off<D>(key, gq));
-                    vw[x][0] = w.x;
-                    vw[x][1] = w.y;
-                    vw[x][2] = w.z;
-                    vw[x][3] = w.w;
+                    vw[k][0] = w.x;
+                    vw[k][1] = w.y;
+                    vw[k][2] = w.z;
+                    vw[k][3] = w.w;
                 } else {
                     const uint2 w = *reinterpret_cast<const uint2 *>(
                         vt + d8_off<D>(key, gq >> 1) + (gq & 1) * 8);
-                    vw[x][0] = w.x;
-                    vw[x][1] = w.y;
+                    vw[k][0] = w.x;
+                    vw[k][1] = w.y;
                 }
             }
             if (!all) {
                 // rows that are not visible hold anything, NaN included: 0 weight times 0
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (!visible(x >> 1, 2 * tq + (x & 1)))
+                for (int k = 0; k < 4; ++k)
+                    if (!visible(x, k >> 1, 2 * tq + (k & 1)))
 #pragma unroll
-                        for (int w = 0; w < kW; ++w) vw[x][w] = 0u;
+                        for (int w = 0; w < kW; ++w) vw[k][w] = 0u;
             }
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);   // elements 0, 1
-                const uint32_t a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);   // elements 2, 3
-                const uint32_t c0 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-                const uint32_t c1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-                const uint32_t b[4][2] = {{lo_f16x2<kInt8>(a0), lo_f16x2<kInt8>(c0)},
-                                          {hi_f16x2<kInt8>(a0), hi_f16x2<kInt8>(c0)},
-                                          {lo_f16x2<kInt8>(a1), lo_f16x2<kInt8>(c1)},
-                                          {hi_f16x2<kInt8>(a1), hi_f16x2<kInt8>(c1)}};
+            for (int w = 0; w < kW; ++w)
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
+                for (int h = 0; h < 2; ++h) {       // elements 4 w + 2 h, 4 w + 2 h + 1
+                    const uint32_t sel = h ? 0x7362 : 0x5140;
+                    uint32_t a[4];
+                    to_f16x2<kInt8>(__byte_perm(vw[0][w], vw[1][w], sel), a[0], a[1]);
+                    to_f16x2<kInt8>(__byte_perm(vw[2][w], vw[3][w], sel), a[2], a[3]);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_16816_f16(oacc[mb][4 * w + x], pa[mb], b[x][0], b[x][1]);
-            }
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816_f16(oacc[nt][2 * w + h], a, pb[nt][x][0], pb[nt][x][1]);
+                }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty_bar[st]);
+        __syncwarp();                               // the slot is read: refill it
+        if (issued < n_iter) issue(issued++);
     }
+    // after a time-out, the copies in flight land before the block exits
+    if (abort_flag)
+        for (int u = max(0, issued - kD8Stages); u < issued; ++u)
+            mbar_wait(&full_bar[warp][u % kD8Stages], (u / kD8Stages) & 1, &abort_flag, p.status, 1000000ull);
 
     // ---- merge the four warps' partial softmax states ----
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            l_run[mb][h] += __shfl_xor_sync(0xffffffffu, l_run[mb][h], 1);
-            l_run[mb][h] += __shfl_xor_sync(0xffffffffu, l_run[mb][h], 2);
+            l_run[nt][h] += __shfl_xor_sync(0xffffffffu, l_run[nt][h], 4);
+            l_run[nt][h] += __shfl_xor_sync(0xffffffffu, l_run[nt][h], 8);
+            l_run[nt][h] += __shfl_xor_sync(0xffffffffu, l_run[nt][h], 16);
         }
-    named_barrier_sync(1, kD8Warps * 32);           // every stage consumed: reuse the ring
+    __syncthreads();                                // every tile consumed: reuse the rings
     constexpr int kRows = Lay::kRows, kStride = Lay::kRowFloats;
     float *s_o = reinterpret_cast<float *>(smem);             // [warp][row][kStride]
     float *s_m = s_o + kD8Warps * kRows * kStride;            // [warp][row]
     float *s_l = s_m + kD8Warps * kRows;                      // [warp][row]
-    auto column = [](int c) { return c + 4 * (c / (D / 4)); };
+    auto column = [](int c) { return c + 4 * (c / (D / 8)); };
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = mb * 16 + gq + ((e >> 1) << 3);
-            float *dst = s_o + (warp * kRows + r) * kStride + column((D / 8) * (2 * tq + (e & 1)));
+        for (int h = 0; h < 2; ++h) {
+            const int r = nt * 8 + 2 * tq + h;
+            float *dst = s_o + (warp * kRows + r) * kStride + column((D / 8) * gq);
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 4)
-                *reinterpret_cast<float4 *>(dst + j) =
-                    make_float4(oacc[mb][j][e] * vref, oacc[mb][j + 1][e] * vref,
-                                oacc[mb][j + 2][e] * vref, oacc[mb][j + 3][e] * vref);
-        }
-        if (tq == 0) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = mb * 16 + gq + h * 8;
-                s_m[warp * kRows + r] = m_run[mb][h];
-                s_l[warp * kRows + r] = l_run[mb][h];
+            for (int j = 0; j < D / 16; j += 2)
+                *reinterpret_cast<float4 *>(dst + 2 * j) =
+                    make_float4(oacc[nt][j][h] * vref, oacc[nt][j][h + 2] * vref,
+                                oacc[nt][j + 1][h] * vref, oacc[nt][j + 1][h + 2] * vref);
+            if (gq == 0) {
+                s_m[warp * kRows + r] = m_run[nt][h];
+                s_l[warp * kRows + r] = l_run[nt][h];
             }
         }
-    }
-    named_barrier_sync(1, kD8Warps * 32);
+    __syncthreads();
     const size_t plane = static_cast<size_t>(p.B) * p.Hq;
-    for (int idx = threadIdx.x; idx < G * D / 4; idx += kD8Warps * 32) {
+    for (int idx = threadIdx.x; idx < G * D / 4; idx += kD8Threads) {
         const int r = idx / (D / 4), c = idx % (D / 4) * 4;
         float M = -INFINITY;
 #pragma unroll
@@ -542,7 +555,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // ---- the last split of this (sequence, K/V head) merges all of them ----
     // Arrival word: see decode.cu (call id and arrivals of that call).
     __threadfence();                                 // my partial rows, device-wide
-    named_barrier_sync(1, kD8Warps * 32);
+    __syncthreads();
     if (threadIdx.x == 0) {
         unsigned long long *word = p.arrivals + static_cast<size_t>(b) * p.Hkv + kvh;
         unsigned long long cur = *reinterpret_cast<volatile unsigned long long *>(word), was, next;
@@ -555,7 +568,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (last) *reinterpret_cast<volatile unsigned long long *>(word) = p.call_id << 16;
         merger = last;
     }
-    named_barrier_sync(1, kD8Warps * 32);
+    __syncthreads();
     if (!merger) return;
     __threadfence();                                 // every split's partial rows are visible
     // One warp per head row; D / 4 lanes hold a row's columns, and the other half
@@ -635,11 +648,11 @@ struct D8Workspace {
     }
 };
 
-template <int D, int MB, bool kInt8, bool kRope>
+template <int D, int NT, bool kInt8, bool kRope>
 static int launch_decode8_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const D8Params &p,
                                  cudaStream_t stream) {
-    auto kern = decode8_kernel<D, MB, kInt8, kRope>;
-    const int smem = D8Layout<D, MB>::kSmemBytes;
+    auto kern = decode8_kernel<D, NT, kInt8, kRope>;
+    const int smem = D8Layout<D, NT>::kSmemBytes;
     static CtxSlot setup;   // one per instantiation: the opt-in is set once per context
     if (int rc = once_per_context(setup, [&](int) {
             return check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -650,14 +663,14 @@ static int launch_decode8_kernel(const CUtensorMap &tk, const CUtensorMap &tv, c
     return check_cuda(cudaGetLastError(), "decode8_kernel launch");
 }
 
-template <int D, int MB>
+template <int D, int NT>
 static int launch_decode8_kind(bool int8, bool rope, const CUtensorMap &tk, const CUtensorMap &tv,
                                const D8Params &p, cudaStream_t s) {
     if (int8)
-        return rope ? launch_decode8_kernel<D, MB, true, true>(tk, tv, p, s)
-                    : launch_decode8_kernel<D, MB, true, false>(tk, tv, p, s);
-    return rope ? launch_decode8_kernel<D, MB, false, true>(tk, tv, p, s)
-                : launch_decode8_kernel<D, MB, false, false>(tk, tv, p, s);
+        return rope ? launch_decode8_kernel<D, NT, true, true>(tk, tv, p, s)
+                    : launch_decode8_kernel<D, NT, true, false>(tk, tv, p, s);
+    return rope ? launch_decode8_kernel<D, NT, false, true>(tk, tv, p, s)
+                : launch_decode8_kernel<D, NT, false, false>(tk, tv, p, s);
 }
 
 }  // namespace gqa
@@ -724,7 +737,7 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     p.page = page;
     p.block = block;
     p.nblk = page / block;
-    p.box = page % 64 == 0 ? 64 : (page % 32 == 0 ? 32 : 16);
+    p.box = page % kD8Keys == 0 ? kD8Keys : 16;
     // a windowed sequence reads the tiles of its sinks and of its window
     long long tiles = d8_tiles(static_cast<long long>(M) * page);
     if (window > 0 && d8_tiles(window) + 1 + d8_tiles(sinks) < tiles)
@@ -740,9 +753,12 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     if (int rc = encode_tmap_rows128(&tv, v_cache, rows, p.box * d / 128)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool int8 = kind == GQA_INT8, rope = theta > 0.0f;
+    const int G = Hq / Hkv;
     if (d == 128)
-        return Hq / Hkv <= 16 ? launch_decode8_kind<128, 1>(int8, rope, tk, tv, p, s)
-                              : launch_decode8_kind<128, 2>(int8, rope, tk, tv, p, s);
-    return Hq / Hkv <= 16 ? launch_decode8_kind<64, 1>(int8, rope, tk, tv, p, s)
-                          : launch_decode8_kind<64, 2>(int8, rope, tk, tv, p, s);
+        return G <= 8    ? launch_decode8_kind<128, 1>(int8, rope, tk, tv, p, s)
+               : G <= 16 ? launch_decode8_kind<128, 2>(int8, rope, tk, tv, p, s)
+                         : launch_decode8_kind<128, 4>(int8, rope, tk, tv, p, s);
+    return G <= 8    ? launch_decode8_kind<64, 1>(int8, rope, tk, tv, p, s)
+           : G <= 16 ? launch_decode8_kind<64, 2>(int8, rope, tk, tv, p, s)
+                     : launch_decode8_kind<64, 4>(int8, rope, tk, tv, p, s);
 }

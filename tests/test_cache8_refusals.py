@@ -137,7 +137,7 @@ def test_workspace_sizes(gqa_lib):
 
 def split_tiles(n, rows, most):
     """The kernel's split rule, restated: tiles per split of n tiles."""
-    t = min(max(-(-n * rows // 444), 2), 16)
+    t = min(max(-(-n * rows // 444), 4), 32)
     per = max(t, -(-n // most))
     splits = -(-n // per)
     return -(-n // splits) if splits else 1
@@ -146,16 +146,16 @@ def split_tiles(n, rows, most):
 @pytest.mark.parametrize("B,Hkv", [(1, 1), (1, 8), (2, 8), (3, 5), (64, 8), (64, 1), (5, 32), (444, 1), (1000, 8)])
 @pytest.mark.parametrize("tiles", [1, 2, 3, 33, 128, 1000, 2048, 16384])
 def test_every_length_fits_its_splits(B, Hkv, tiles):
-    # a table of `tiles` tiles: no sequence needs more splits than the workspace
-    # and grid have, nor more tiles a split than the kernel's arrays (16)
+    # a table of `tiles` 32-key tiles: no sequence needs more splits than the
+    # workspace and grid have, nor more tiles a split than its warps can hold (32)
     rows = B * Hkv
-    most = max(-(-tiles // 16), min(-(-444 // rows), -(-tiles // 2)))
+    most = max(-(-tiles // 32), min(-(-444 // rows), -(-tiles // 4)))
     need = 2 * Hkv * B * (64 + 1) * 4                   # Hq = 2 Hkv, d = 64
-    got = b.gqa_decode8_workspace_size(B, 2 * Hkv, Hkv, 64, tiles * 64)
+    got = b.gqa_decode8_workspace_size(B, 2 * Hkv, Hkv, 64, tiles * 32)
     assert (got == 0) == (most == 1) and got >= most * need * (most > 1)
     for n in {*range(1, min(tiles, 300) + 1), *range(max(1, tiles - 50), tiles + 1)}:
         per = split_tiles(n, rows, most)
-        assert 1 <= per <= 16 and -(-n // per) <= most
+        assert 1 <= per <= 32 and -(-n // per) <= most
 
 
 def test_wrappers_refuse_host_tensors():
