@@ -417,7 +417,7 @@ size_t gqa_decode8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax);
  *   exist).  theta: 0 for none, else q is rotated as it is loaded, at position
  *   max(seqlens[b] - 1, 0), with gqa_rope_decode_q's arithmetic (the cached keys
  *   are rotated before they are appended).
- * Hq % Hkv == 0, Hq / Hkv <= 32 (else UNSUPPORTED), B and Hkv <= 65535.
+ * Hq % Hkv == 0, Hq / Hkv <= 32 (else UNSUPPORTED).
  * workspace: >= gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page) bytes,
  * 256-byte aligned, contents on entry irrelevant; calls in flight at the same
  * time (other streams, captured graphs) need workspaces of their own.

@@ -1,6 +1,8 @@
 """The paged 8-bit cache at the C boundary and in the Python wrappers: what is
 refused before any CUDA call (no GPU needed)."""
 
+import random
+
 import pytest
 import torch
 
@@ -96,7 +98,7 @@ def test_rows(gqa_lib, call, kw, code):
     (dict(Hq=7), BAD), (dict(Hq=0), BAD), (dict(Hq=66), UNS), (dict(scale=0.0), BAD),
     (dict(scale=float("nan")), BAD), (dict(theta=-1.0), BAD), (dict(theta=float("inf")), BAD),
     (dict(window=-1), BAD), (dict(sinks=-1), BAD), (dict(q=None), BAD), (dict(o=FAKE + 8), BAD),
-    (dict(B=65536), UNS), (dict(ws=None), WS), (dict(ws=FAKE + 16), WS), (dict(ws_bytes=64), WS),
+    (dict(ws=None), WS), (dict(ws=FAKE + 16), WS), (dict(ws_bytes=64), WS),
     (dict(B=0, q=None, ws=None), OK)])
 def test_decode8(gqa_lib, kw, code):
     assert decode8(**kw) == code
@@ -129,33 +131,34 @@ def test_codes_match_the_header():
 def test_workspace_sizes(gqa_lib):
     size = b.gqa_decode8_workspace_size
     n = size(64, 32, 8, 128, 8192)
-    assert n > 0 and n % 256 == 0 and size(64, 32, 8, 128, 16384) > n
-    assert size(64, 32, 8, 128, 1) == 0                 # one split: no partial results
+    assert n > 0 and n % 256 == 0 and size(64, 32, 8, 128, 16384) == n
+    assert size(1, 32, 1, 128, 128) == 0                # one CTA: no partial results
     assert size(64, 32, 3, 128, 8192) == 0 and size(-1, 32, 8, 128, 8192) == 0
     assert b.gqa_pages_workspace_size(4, 4, 16) % 256 == 0 and b.gqa_pages_workspace_size(4, 0, 16) == 0
 
 
-def split_tiles(n, rows, most):
-    """The kernel's split rule, restated: tiles per split of n tiles."""
-    t = min(max(-(-n * rows // 444), 4), 32)
-    per = max(t, -(-n // most))
-    splits = -(-n // per)
-    return -(-n // splits) if splits else 1
-
-
-@pytest.mark.parametrize("B,Hkv", [(1, 1), (1, 8), (2, 8), (3, 5), (64, 8), (64, 1), (5, 32), (444, 1), (1000, 8)])
-@pytest.mark.parametrize("tiles", [1, 2, 3, 33, 128, 1000, 2048, 16384])
-def test_every_length_fits_its_splits(B, Hkv, tiles):
-    # a table of `tiles` 32-key tiles: no sequence needs more splits than the
-    # workspace and grid have, nor more tiles a split than its warps can hold (32)
-    rows = B * Hkv
-    most = max(-(-tiles // 32), min(-(-444 // rows), -(-tiles // 4)))
-    need = 2 * Hkv * B * (64 + 1) * 4                   # Hq = 2 Hkv, d = 64
-    got = b.gqa_decode8_workspace_size(B, 2 * Hkv, Hkv, 64, tiles * 32)
-    assert (got == 0) == (most == 1) and got >= most * need * (most > 1)
-    for n in {*range(1, min(tiles, 300) + 1), *range(max(1, tiles - 50), tiles + 1)}:
-        per = split_tiles(n, rows, most)
-        assert 1 <= per <= 32 and -(-n // per) <= most
+@pytest.mark.parametrize("B,Hkv,G", [(1, 1, 1), (1, 8, 4), (3, 5, 7), (64, 8, 4), (1000, 8, 32)])
+@pytest.mark.parametrize("tiles", [1, 4, 5, 33, 1000, 16384])
+def test_workspace_covers_every_cut(gqa_lib, B, Hkv, G, tiles):
+    # the tiles of all (sequence, head) units in equal runs of at least 4 tiles, one
+    # per CTA, at most 444 CTAs: each CTA writes at most two pieces of G rows
+    got = b.gqa_decode8_workspace_size(B, G * Hkv, Hkv, 64, tiles * 32)
+    ctas = min(444, -(-tiles * B * Hkv // 4))
+    assert got >= (ctas > 1) * (ctas * 2 * G * (64 + 1) * 4 + B * Hkv * 8)
+    rng = random.Random(tiles + B)
+    for _ in range(20):
+        n = [rng.choice([0, 1, tiles, rng.randint(0, tiles)]) for _ in range(min(B, 40)) for _ in range(Hkv)]
+        per = max(4, -(-sum(n) // ctas))
+        assert -(-sum(n) // per) <= ctas
+        at = 0
+        begun, carried = [0] * ctas, [0] * ctas
+        for x in n:
+            if x and at // per != (at + x - 1) // per:
+                begun[at // per] += 1
+                for c in range(at // per + 1, (at + x - 1) // per + 1):
+                    carried[c] += 1
+            at += x
+        assert max(begun) <= 1 and max(carried) <= 1     # one slot each
 
 
 def test_wrappers_refuse_host_tensors():
