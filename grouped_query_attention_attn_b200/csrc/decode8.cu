@@ -44,7 +44,7 @@
 //
 // A unit that lies in one CTA's run is written by it.  Otherwise its pieces go to
 // the workspace, and the last one to arrive merges them with the log-sum-exp
-// identity; the arrival words are those of decode.cu.
+// identity.
 #include <cmath>
 
 #include "cache8.cuh"
@@ -57,6 +57,7 @@ constexpr int kD8Threads = kD8Warps * 32;
 constexpr int kD8Epoch = 16;                       // tiles whose pages a warp's lanes hold
 constexpr int kD8MinTiles = kD8Warps;              // shortest run of a CTA
 constexpr int kD8MaxCtas = 444;                    // 148 SMs x 3 resident CTAs
+constexpr float kD8Least = -3.0e38f;               // reference of a row that has seen no key
 constexpr float kD8Rescale = 8.0f;                 // log2 units: weights stay below 2^8
 
 struct D8Params {
@@ -142,6 +143,23 @@ __device__ __forceinline__ void lds(uint32_t (&r)[2], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]) : "r"(addr), "n"(kOff));
 }
 
+// tma_load_2d of whole 128-byte rows with 32-bit shared-memory addresses.
+// The cache is read once: it should not push the tables, scales and partial results
+// out of L2.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void copy_rows(uint32_t dst, const void *tmap, uint32_t bar, int row,
+                                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;"
+        ::"r"(dst), "l"(tmap), "r"(bar), "r"(0), "r"(row), "l"(policy)
+        : "memory");
+}
+
 // Transpose of an 8 x 8 matrix of f16 held one pair per lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t y;
@@ -208,8 +226,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
             off += __shfl_sync(0xffffffffu, x, 31);
         }
-    uint8_t *ring = smem + warp * Lay::kRingBytes;
-    const uint32_t ring_addr = smem_u32(ring);
+    const uint64_t policy = evict_first_policy();
+    const uint32_t ring_addr = smem_u32(smem + warp * Lay::kRingBytes), bar_addr = smem_u32(full_bar[warp]);
     // where this thread reads a tile: K key d8_key(nb, gq), V key d8_key(k >> 1, 2 tq + (k & 1))
     uint32_t k_off[2][D / 64], v_off[4];
 #pragma unroll
@@ -251,7 +269,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         };
         // Lane i holds what is known of the 16 keys that are half i & 1 of tile i >> 1 of
         // an epoch: their first row in the cache (-1: not there; fits an int, checked on
-        // the host), its place in the page, and the scales (V scale -1: not there).
+        // the host), its place in the page, and the scales.  The V scale is negated where
+        // some of the keys are out of sight, and -inf where none is there.
         struct Group {
             int row, off;
             float ks, vs;
@@ -269,44 +288,53 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     record_status(p.status, GQA_ERR_INVALID_ARG);
             }
         };
-        auto load_scales = [&](Group &g) {
+        auto load_scales = [&](int epoch, Group &g) {
             g.ks = 0.0f;
-            g.vs = -1.0f;
+            g.vs = -INFINITY;
             if (g.row >= 0) {
                 const size_t at = static_cast<size_t>((g.row - g.off) / p.page) * p.nblk + g.off / p.block;
+                const int key = key_of(epoch * kD8Epoch + (lane >> 1)) + (lane & 1) * 16;
                 g.ks = p.k_scale[at];
                 g.vs = p.v_scale[at];
+                if (!(key + 16 <= L && (key >= seq.lo || key + 16 <= seq.sinks))) g.vs = -g.vs;
             }
         };
-        // Copies of tile t into ring slot sl, counted on the slot's barrier; rows: the
-        // lanes' rows in t's epoch.
-        auto issue = [&](int t, int sl, int rows) {
-            const int r0 = __shfl_sync(0xffffffffu, rows, (2 * t) & 31);
-            const int r1 = __shfl_sync(0xffffffffu, rows, (2 * t + 1) & 31);
-            if (lane == 0) {
-                uint64_t *bar = &full_bar[warp][sl];
-                uint8_t *kt = ring + sl * Lay::kStageBytes;
-                uint8_t *vt = kt + Lay::kTileBytes;
+        // Copies of tile t into ring slot sl, counted on the slot's barrier, by the lane
+        // that holds the tile's first half; g: the groups of t's epoch.
+        auto issue = [&](int t, int sl, int row0) {
+            const int row1 = __shfl_down_sync(0xffffffffu, row0, 1);
+            if (lane == (2 * t & 31)) {
+                const uint32_t bar = bar_addr + sl * 8, kt = ring_addr + sl * Lay::kStageBytes;
                 if (p.box == kD8Keys) {             // both halves lie in one page
-                    const int r = r0 >= 0 ? r0 : r1 - 16;
-                    mbar_expect_tx(bar, r1 >= 0 || r0 >= 0 ? Lay::kStageBytes : 0);
-                    if (r1 >= 0 || r0 >= 0) {
-                        tma_load_2d(kt, &tm_k, bar, 0, r / (128 / D));
-                        tma_load_2d(vt, &tm_v, bar, 0, r / (128 / D));
+                    const int r = max(row0, row1 - 16);
+                    const bool there = max(row0, row1) >= 0;
+                    mbar_expect_tx(&full_bar[warp][sl], there ? Lay::kStageBytes : 0);
+                    if (there) {
+                        copy_rows(kt, &tm_k, bar, r / (128 / D), policy);
+                        copy_rows(kt + Lay::kTileBytes, &tm_v, bar, r / (128 / D), policy);
                     }
                 } else {
-                    mbar_expect_tx(bar, ((r0 >= 0) + (r1 >= 0)) * (Lay::kStageBytes / 2));
+                    mbar_expect_tx(&full_bar[warp][sl],
+                                   ((row0 >= 0) + (row1 >= 0)) * (Lay::kStageBytes / 2));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int r = x ? r1 : r0;
+                        const int r = x ? row1 : row0;
                         if (r < 0) continue;
-                        tma_load_2d(kt + x * (Lay::kTileBytes / 2), &tm_k, bar, 0, r / (128 / D));
-                        tma_load_2d(vt + x * (Lay::kTileBytes / 2), &tm_v, bar, 0, r / (128 / D));
+                        const uint32_t dst = kt + x * (Lay::kTileBytes / 2);
+                        copy_rows(dst, &tm_k, bar, r / (128 / D), policy);
+                        copy_rows(dst + Lay::kTileBytes, &tm_v, bar, r / (128 / D), policy);
                     }
                 }
             }
             __syncwarp();
         };
+        // Arrival word of a unit in several pieces: call id in the high 48 bits, arrivals
+        // in the low 16.  Every piece claims the word for this call before it starts
+        // (whatever another call, or uninitialised memory, left there; if the exchange
+        // fails, another piece has claimed it), so that an arrival is one addition.  The
+        // last one leaves (call id, 0) for a replay of the same launch.
+        unsigned long long *word = p.arrivals + unit, left = 0;
+        if (threadIdx.x == 0 && cta0 != cta1) left = *reinterpret_cast<volatile unsigned long long *>(word);
         // Loads that nothing waits for yet come first: once the copies of all CTAs are
         // under way, a load takes several microseconds.
         Group cur, next;
@@ -317,7 +345,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         constexpr int kQ = D / 4;
         const __nv_bfloat16 *qg = p.q + grow0 * D + tq * kQ;
         uint32_t qb[NT][D / 16][2];
-        float qs[NT][2];                                // score scale of heads 2 tq, 2 tq + 1
+        float2 qs[NT];                                  // score scale of heads 2 tq, 2 tq + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * 8 + gq;
@@ -341,9 +369,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 rope_cs[i] = make_float2(cs, sn);
             }
         }
-        load_scales(cur);
+        load_scales(0, cur);
         for (int t = 0; t < min(n_iter, kStages); ++t)
             issue(t, st + t < kStages ? st + t : st + t - kStages, cur.row);
+        if (threadIdx.x == 0 && cta0 != cta1 && (left >> 16) != p.call_id)
+            atomicCAS(word, left, p.call_id << 16);
         if constexpr (kRope) {
             __syncthreads();
 #pragma unroll
@@ -373,8 +403,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const uint32_t ex = min(e, 253);            // 2^(ex - 127) and its inverse are normal
             const float up = fit ? __uint_as_float((254 - ex) << 23) : 1.0f;
             const float down = (fit ? __uint_as_float(ex << 23) : 1.0f) * p.scale_log2;
-            qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * tq);
-            qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * tq + 4);
+            qs[nt].x = __shfl_sync(0xffffffffu, down, 8 * tq);
+            qs[nt].y = __shfl_sync(0xffffffffu, down, 8 * tq + 4);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
 #pragma unroll
@@ -385,16 +415,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         // O^T: product j, accumulator e is element (D / 8) gq + 2 j + (e >> 1) of head 2 tq + (e & 1)
         float oacc[NT][D / 16][4];
-        float m_ref[NT][2], l_run[NT][2];
-        float vref = 0.0f, vinv = 0.0f;                 // O is in units of vref (0: O is still 0)
+        float2 m_ref[NT], l_run[NT];                    // of heads 2 tq, 2 tq + 1
+        float vref = -1.0f, vinv = 0.0f;                // O is in units of vref (-1: O is still 0)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) oacc[nt][j][e] = 0.0f;
-            m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
-            l_run[nt][0] = l_run[nt][1] = 0.0f;
+            m_ref[nt] = make_float2(kD8Least, kD8Least);
+            l_run[nt] = make_float2(0.0f, 0.0f);
         }
 
         bool ok = true;
@@ -404,9 +434,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[warp][st], ph, &abort_flag[warp], p.status));
             if (!ok) break;
             const uint32_t kt = ring_addr + st * Lay::kStageBytes;
-            const int key0 = key_of(t);
             // the next epoch's rows are loaded one epoch ahead, its scales half of one
-            if (t % kD8Epoch == kD8Epoch / 2) load_scales(next);
+            if (t % kD8Epoch == kD8Epoch / 2) load_scales(t / kD8Epoch + 1, next);
             if (t % kD8Epoch == 0 && t > 0) {
                 cur = next;
                 load_rows(t / kD8Epoch + 1, next);
@@ -444,104 +473,106 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             mma_16816_f16(sacc[nt][x], a, qb[nt][c * 4 + i][0], qb[nt][c * 4 + i][1]);
                     }
             }
-            // ---- V scales: weight factor of each half, and O's change of units before it ----
+            // ---- V scales: weight factor of each half, and O's change of units before it;
+            //      keys out of sight: a bit of hide_k for half x, key (nb, gq) at 2 x + nb, of
+            //      hide_v for its key (k >> 1, 2 tq + (k & 1)) at 4 x + k ----
             float pscale[2], ratio[2] = {1.0f, 1.0f};
+            uint32_t hide_k = 0, hide_v = 0;
             if (vs[0] <= vref && vs[0] * 64.0f >= vref && vs[1] <= vref && vs[1] * 64.0f >= vref) {
-                pscale[0] = vs[0] * vinv;
+                pscale[0] = vs[0] * vinv;           // all in sight: vref is positive or -1
                 pscale[1] = vs[1] * vinv;
             } else {
+                const int key0 = key_of(t);
+                auto hidden = [&](int x, int nb, int n) -> uint32_t {
+                    const int key = key0 + x * 16 + d8_key<D>(nb, n);
+                    return vs[x] == -INFINITY || key >= L || (key < seq.lo && key >= seq.sinks);
+                };
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
+                    if (signbit(vs[x])) {
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb) hide_k |= hidden(x, nb, gq) << (2 * x + nb);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            hide_v |= hidden(x, k >> 1, 2 * tq + (k & 1)) << (4 * x + k);
+                    }
+                    const float v = fabsf(vs[x]);
                     pscale[x] = 0.0f;               // scale 0, or not there
-                    if (vs[x] == 0.0f || vs[x] == -1.0f) continue;
-                    if (!(vs[x] <= vref && vs[x] * 64.0f >= vref)) {
-                        const float nv = fmaxf(vs[x], vref * 5.42101086e-20f);      // 2^-64
+                    if (v == 0.0f || vs[x] == -INFINITY) continue;
+                    if (!(v <= vref && v * 64.0f >= vref)) {
+                        const float nv = fmaxf(v, vref * 5.42101086e-20f);          // 2^-64
                         if (vref > 0.0f) ratio[x] = vref / nv;
                         vref = nv;
                         vinv = 1.0f / nv;
                     }
-                    pscale[x] = vs[x] * vinv;
+                    pscale[x] = v * vinv;
                 }
             }
-            // ---- scores; keys out of sight get -inf ----
-            const bool all = key0 + kD8Keys <= L && (key0 >= seq.lo || key0 + kD8Keys <= seq.sinks) &&
-                             vs[0] != -1.0f && vs[1] != -1.0f;
-            auto visible = [&](int x, int nb, int n) {
-                const int key = key0 + x * 16 + d8_key<D>(nb, n);
-                return vs[x] != -1.0f && key < L && (key >= seq.lo || key < seq.sinks);
-            };
+            float2 f[NT][2];                        // factor of the scores of heads 2 tq, 2 tq + 1
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float f0 = qs[nt][0] * ks[x], f1 = qs[nt][1] * ks[x];
-                    sacc[nt][x][0] *= f0;
-                    sacc[nt][x][1] *= f1;
-                    sacc[nt][x][2] *= f0;
-                    sacc[nt][x][3] *= f1;
-                }
-            if (!all) {
+                for (int x = 0; x < 2; ++x) f[nt][x] = mul2(qs[nt], make_float2(ks[x], ks[x]));
+            if (hide_k) {
+                // -inf must stay so whatever its factor: the scores are scaled here
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-                        const bool out = !visible(x, nb, gq);
+                    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            sacc[nt][x][2 * nb] = out ? -INFINITY : sacc[nt][x][2 * nb];
-                            sacc[nt][x][2 * nb + 1] = out ? -INFINITY : sacc[nt][x][2 * nb + 1];
+                        for (int e = 0; e < 4; ++e) {
+                            sacc[nt][x][e] *= e & 1 ? f[nt][x].y : f[nt][x].x;
+                            if (hide_k >> (2 * x + (e >> 1)) & 1) sacc[nt][x][e] = -INFINITY;
                         }
+                        f[nt][x] = make_float2(1.0f, 1.0f);
                     }
             }
             // ---- softmax: the reference m only moves when a score passes it by more than
             //      kD8Rescale, so that O and l are seldom rescaled ----
             auto rescale = [&](int nt, float f0, float f1) {
+                const float2 f = make_float2(f0, f1);
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    oacc[nt][j][0] *= f0;
-                    oacc[nt][j][1] *= f1;
-                    oacc[nt][j][2] *= f0;
-                    oacc[nt][j][3] *= f1;
-                }
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2) {
+                        const float2 o = mul2(make_float2(oacc[nt][j][h], oacc[nt][j][h + 1]), f);
+                        oacc[nt][j][h] = o.x;
+                        oacc[nt][j][h + 1] = o.y;
+                    }
             };
             uint32_t pb[NT][2][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float(&s)[2][4] = sacc[nt];
+                const float(&s)[2][4] = sacc[nt];
                 float mx[2];
+                mx[0] = fmaxf(fmaxf(s[0][0], s[0][2]) * f[nt][0].x, fmaxf(s[1][0], s[1][2]) * f[nt][1].x);
+                mx[1] = fmaxf(fmaxf(s[0][1], s[0][3]) * f[nt][0].y, fmaxf(s[1][1], s[1][3]) * f[nt][1].y);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    mx[h] = fmaxf(max3f(s[0][h], s[0][h + 2], s[1][h]), s[1][h + 2]);
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 4));
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 8));
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
                 }
-                if (__any_sync(0xffffffffu, mx[0] > m_ref[nt][0] + kD8Rescale ||
-                                                mx[1] > m_ref[nt][1] + kD8Rescale)) {
-                    float alpha[2];
+                if (__any_sync(0xffffffffu, mx[0] > m_ref[nt].x + kD8Rescale ||
+                                                mx[1] > m_ref[nt].y + kD8Rescale)) {
+                    const float2 m = make_float2(fmaxf(m_ref[nt].x, mx[0]), fmaxf(m_ref[nt].y, mx[1]));
+                    const float2 alpha = make_float2(fast_exp2(m_ref[nt].x - m.x),
+                                                     fast_exp2(m_ref[nt].y - m.y));
+                    m_ref[nt] = m;
+                    l_run[nt] = mul2(l_run[nt], alpha);
+                    rescale(nt, alpha.x, alpha.y);
+                }
+                const float2 minus_m = make_float2(-m_ref[nt].x, -m_ref[nt].y);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float m = fmaxf(m_ref[nt][h], mx[h]);
-                        alpha[h] = m == -INFINITY ? 1.0f : fast_exp2(m_ref[nt][h] - m);
-                        m_ref[nt][h] = m;
-                        l_run[nt][h] *= alpha[h];
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+                        float2 w = fma2(make_float2(s[x][2 * nb], s[x][2 * nb + 1]), f[nt][x], minus_m);
+                        w = make_float2(fast_exp2(w.x), fast_exp2(w.y));
+                        l_run[nt] = add2(l_run[nt], w);
+                        w = mul2(w, make_float2(pscale[x], pscale[x]));
+                        pb[nt][x][nb] = transpose_8x8(pack_f16x2(w.x, w.y));
                     }
-                    rescale(nt, alpha[0], alpha[1]);
-                }
-                // a row that has seen no key yet: every score is -inf, every weight 0
-                const float m0 = m_ref[nt][0] == -INFINITY ? 0.0f : m_ref[nt][0];
-                const float m1 = m_ref[nt][1] == -INFINITY ? 0.0f : m_ref[nt][1];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    s[x][0] = fast_exp2(s[x][0] - m0);
-                    s[x][1] = fast_exp2(s[x][1] - m1);
-                    s[x][2] = fast_exp2(s[x][2] - m0);
-                    s[x][3] = fast_exp2(s[x][3] - m1);
-                    pb[nt][x][0] = transpose_8x8(pack_f16x2(s[x][0] * pscale[x], s[x][1] * pscale[x]));
-                    pb[nt][x][1] = transpose_8x8(pack_f16x2(s[x][2] * pscale[x], s[x][3] * pscale[x]));
-                }
-                l_run[nt][0] += (s[0][0] + s[0][2]) + (s[1][0] + s[1][2]);
-                l_run[nt][1] += (s[0][1] + s[0][3]) + (s[1][1] + s[1][3]);
             }
             // ---- O^T += V^T P^T ----
             constexpr int kW = D / 32;              // words of V per key and thread
@@ -551,16 +582,15 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 lds<Lay::kTileBytes>(vw[0][k], kt + v_off[k]);
                 lds<Lay::kTileBytes + 16 * D>(vw[1][k], kt + v_off[k]);
             }
-            if (!all) {
-                // rows that are not visible hold anything, NaN included: 0 weight times 0
+            if (hide_v) {
+                // rows out of sight hold anything, NaN included: 0 weight times 0
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const bool out = !visible(x, k >> 1, 2 * tq + (k & 1));
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int w = 0; w < kW; ++w) vw[x][k][w] = out ? 0u : vw[x][k][w];
-                    }
+                        for (int w = 0; w < kW; ++w)
+                            if (hide_v >> (4 * x + k) & 1) vw[x][k][w] = 0u;
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -602,11 +632,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l_run[nt][h] += __shfl_xor_sync(0xffffffffu, l_run[nt][h], 4);
-                l_run[nt][h] += __shfl_xor_sync(0xffffffffu, l_run[nt][h], 8);
-                l_run[nt][h] += __shfl_xor_sync(0xffffffffu, l_run[nt][h], 16);
+            for (int x = 4; x < 32; x <<= 1) {
+                l_run[nt].x += __shfl_xor_sync(0xffffffffu, l_run[nt].x, x);
+                l_run[nt].y += __shfl_xor_sync(0xffffffffu, l_run[nt].y, x);
             }
+        vref = fmaxf(vref, 0.0f);
         __syncthreads();                                // every tile consumed: reuse the rings
         if (abort_flag[0] | abort_flag[1] | abort_flag[2] | abort_flag[3]) return;
         constexpr int kRows = Lay::kRows, kStride = Lay::kRowFloats;
@@ -626,14 +656,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         make_float4(oacc[nt][j][h] * vref, oacc[nt][j][h + 2] * vref,
                                     oacc[nt][j + 1][h] * vref, oacc[nt][j + 1][h + 2] * vref);
                 if (gq == 0) {
-                    s_m[warp * kRows + r] = m_ref[nt][h];
-                    s_l[warp * kRows + r] = l_run[nt][h];
+                    s_m[warp * kRows + r] = h ? m_ref[nt].y : m_ref[nt].x;
+                    s_l[warp * kRows + r] = h ? l_run[nt].y : l_run[nt].x;
                 }
             }
         __syncthreads();
-        // the unit's arrival word, asked for early
-        unsigned long long *word = p.arrivals + unit, now = 0;
-        if (threadIdx.x == 0 && cta0 != cta1) now = *reinterpret_cast<volatile unsigned long long *>(word);
         for (int idx = threadIdx.x; idx < G * D / 4; idx += kD8Threads) {
             const int r = idx / (D / 4), c = idx % (D / 4) * 4;
             float M = -INFINITY;
@@ -643,8 +670,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kD8Warps; ++w) {
-                // 0 for a warp with no key (M is -inf when none has any)
-                const float f = M == -INFINITY ? 0.0f : fast_exp2(s_m[w * kRows + r] - M);
+                const float f = fast_exp2(s_m[w * kRows + r] - M);
                 const float4 x =
                     *reinterpret_cast<const float4 *>(s_o + (w * kRows + r) * kStride + column(c));
                 wsum += f * s_l[w * kRows + r];
@@ -673,18 +699,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
 
         // ---- the last piece of the unit to arrive merges all of them ----
-        // Arrival word: see decode.cu (call id and arrivals of that call).
         __threadfence();                            // my partial rows, device-wide
         __syncthreads();
         const int pieces = cta1 - cta0 + 1;
         if (threadIdx.x == 0) {
-            unsigned long long was, then;
-            do {
-                was = now;
-                then = (was >> 16) == p.call_id ? was + 1 : ((p.call_id << 16) | 1ull);
-                now = atomicCAS(word, was, then);
-            } while (now != was);
-            const bool last = static_cast<int>(then & 0xFFFFu) == pieces;
+            const bool last = static_cast<int>(atomicAdd(word, 1ull) & 0xFFFFu) + 1 == pieces;
             if (last) *reinterpret_cast<volatile unsigned long long *>(word) = p.call_id << 16;
             merger = last;
         }
