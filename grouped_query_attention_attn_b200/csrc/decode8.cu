@@ -7,8 +7,9 @@
 // tiles of all units (sequence, K/V head), one after another, are cut into equal
 // runs, one per CTA, with all CTAs resident at once: ragged lengths, few rows and
 // many rows are balanced alike, a unit is cut into as few pieces as that allows,
-// and a CTA starts and merges about once.  Each CTA sums the tiles of all
-// sequences to find its run.
+// and a CTA starts and merges about once.  In the line of tiles each unit begins
+// with a few empty places, which stand for the time that beginning a unit takes.
+// Each CTA sums the places of all sequences to find its run.
 //
 // The four warps of a CTA take the tiles of a piece in turn, each with a TMA ring
 // of its own: one lane issues a box per page part (32 or 16 keys, whatever divides
@@ -54,6 +55,7 @@ namespace gqa {
 constexpr int kD8Keys = 32;                        // keys per tile
 constexpr int kD8Warps = 4;                        // each takes every fourth tile of a piece
 constexpr int kD8Threads = kD8Warps * 32;
+constexpr int kD8Begin = 12;                       // what beginning a unit costs, in tiles
 constexpr int kD8Epoch = 16;                       // tiles whose pages a warp's lanes hold
 constexpr int kD8MinTiles = kD8Warps;              // shortest run of a CTA
 constexpr int kD8MaxCtas = 444;                    // 148 SMs x 3 resident CTAs
@@ -195,13 +197,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         tma_prefetch_desc(&tm_v);
     }
     __syncwarp();
-    auto tiles_of = [&](int b) {
-        return D8Tiles(min(max(p.seqlens[b], 0), Lmax), p.window, p.sinks).n;
+    // places that each unit of sequence b takes in the line of tiles: kD8Begin empty
+    // ones, then its tiles
+    auto places_of = [&](int b) {
+        const int n = D8Tiles(min(max(p.seqlens[b], 0), Lmax), p.window, p.sinks).n;
+        return n > 0 ? n + kD8Begin : 0;
     };
 
     // ---- this CTA's run of tiles; every warp finds it for itself ----
     int total = 0;                                  // fits an int (checked on the host)
-    for (int b = lane; b < p.B; b += 32) total += tiles_of(b);
+    for (int b = lane; b < p.B; b += 32) total += places_of(b);
     total = __reduce_add_sync(0xffffffffu, total) * p.Hkv;
     const int per = max(kD8MinTiles, (total - 1) / static_cast<int>(gridDim.x) + 1);
     int pos = per * blockIdx.x;
@@ -210,7 +215,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     int b = 0, off = 0;
     if (pos < end)
         for (int b0 = 0;; b0 += 32) {               // ends: pos < total
-            const int n = b0 + lane < p.B ? tiles_of(b0 + lane) * p.Hkv : 0;
+            const int n = b0 + lane < p.B ? places_of(b0 + lane) * p.Hkv : 0;
             int x = n;                              // inclusive prefix sum
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -250,18 +255,21 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             continue;
         }
         // ---- the piece: tiles first .. first + count - 1 of unit (b, kvh) ----
-        const int kvh = (pos - off) / seq.n, first = (pos - off) - kvh * seq.n;
-        const int count = min(seq.n - first, end - pos);
+        const int places = seq.n + kD8Begin, kvh = (pos - off) / places;
+        const int tile0 = off + kvh * places + kD8Begin;         // place of the unit's first tile
+        const int stop = min(tile0 + seq.n, end), first = max(pos - tile0, 0);
+        const int count = stop - (tile0 + first);
         // CTAs whose runs hold the unit's first and last tile
-        const int unit0 = off + kvh * seq.n, cta0 = unit0 / per, cta1 = (unit0 + seq.n - 1) / per;
+        const int cta0 = tile0 / per, cta1 = (tile0 + seq.n - 1) / per;
         const size_t grow0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(kvh) * G;
         const size_t unit = static_cast<size_t>(b) * p.Hkv + kvh;
         const int32_t *row = p.table + static_cast<size_t>(b) * p.M;
-        pos += count;
-        if (kvh == p.Hkv - 1 && first + count == seq.n) {        // on to the next sequence
-            off += p.Hkv * seq.n;
+        pos = stop;                                 // (a run may end in the empty places)
+        if (kvh == p.Hkv - 1 && pos == tile0 + seq.n) {          // on to the next sequence
+            off += p.Hkv * places;
             ++b;
         }
+        if (count <= 0) continue;
         const int n_iter = (count - warp + kD8Warps - 1) / kD8Warps;      // tiles of this warp
         auto key_of = [&](int t) { return seq.tile(first + warp + t * kD8Warps) * kD8Keys; };
         auto seen = [&](int key0, int n) {          // any of n keys visible
@@ -768,7 +776,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int z = blockIdx.x; z < p.B; z += gridDim.x) {
         if (threadIdx.x == 0 && (p.seqlens[z] < 0 || p.seqlens[z] > Lmax))
             record_status(p.status, GQA_ERR_INVALID_ARG);
-        if (tiles_of(z) == 0)
+        if (places_of(z) == 0)
             for (int i = threadIdx.x; i < p.Hq * D / 8; i += kD8Threads)
                 reinterpret_cast<uint4 *>(p.o + static_cast<size_t>(z) * p.Hq * D)[i] =
                     make_uint4(0u, 0u, 0u, 0u);
@@ -779,7 +787,7 @@ static long long d8_tiles(long long keys) { return (keys + kD8Keys - 1) / kD8Key
 
 // CTAs that B sequences of up to `tiles` tiles can keep busy, at most `most`.
 static int d8_grid(int B, int Hkv, long long tiles, int most) {
-    const double runs = ceil(static_cast<double>(tiles) * B * Hkv / kD8MinTiles);
+    const double runs = ceil(static_cast<double>(tiles + kD8Begin) * B * Hkv / kD8MinTiles);
     return runs < most ? static_cast<int>(runs) : most;
 }
 
@@ -793,7 +801,7 @@ struct D8Workspace {
         const size_t ctas = d8_grid(B, Hkv, d8_tiles(Lmax), kD8MaxCtas), rows = ctas * 2 * (Hq / Hkv);
         off_lse = align256(rows * d * sizeof(float));
         off_arrivals = off_lse + align256(rows * sizeof(float));
-        bytes = ctas > 1 ? off_arrivals + align256(static_cast<size_t>(B) * Hkv * 8) : 0;
+        bytes = off_arrivals + align256(static_cast<size_t>(B) * Hkv * 8);
     }
 };
 
@@ -898,7 +906,7 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     if (int rc = encode_tmap_rows128(&tk, k_cache, rows, p.box * d / 128)) return rc;
     if (int rc = encode_tmap_rows128(&tv, v_cache, rows, p.box * d / 128)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (static_cast<double>(tiles) * B * Hkv > 2147483647.0 - kD8MaxCtas)
+    if (static_cast<double>(tiles + kD8Begin) * B * Hkv > 2147483647.0 - kD8MaxCtas)
         return set_error(GQA_ERR_UNSUPPORTED, "decode8: B=%d x Hkv=%d x M=%d x page=%d rows are too many", B,
                          Hkv, M, page);
     const bool int8 = kind == GQA_INT8, rope = theta > 0.0f;

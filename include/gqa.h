@@ -405,7 +405,7 @@ int gqa_cache8_copy(void *k_cache, void *v_cache, float *k_scale, float *v_scale
                     gqa_stream_t stream);
 
 /* Bytes of device scratch gqa_decode8 needs for caches of Lmax = M * page rows a
- * sequence; 0 for invalid sizes or when none is needed.  Pure host function. */
+ * sequence; 0 for invalid sizes.  Pure host function. */
 size_t gqa_decode8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax);
 
 /*

@@ -132,7 +132,6 @@ def test_workspace_sizes(gqa_lib):
     size = b.gqa_decode8_workspace_size
     n = size(64, 32, 8, 128, 8192)
     assert n > 0 and n % 256 == 0 and size(64, 32, 8, 128, 16384) == n
-    assert size(1, 32, 1, 128, 128) == 0                # one CTA: no partial results
     assert size(64, 32, 3, 128, 8192) == 0 and size(-1, 32, 8, 128, 8192) == 0
     assert b.gqa_pages_workspace_size(4, 4, 16) % 256 == 0 and b.gqa_pages_workspace_size(4, 0, 16) == 0
 
@@ -140,19 +139,21 @@ def test_workspace_sizes(gqa_lib):
 @pytest.mark.parametrize("B,Hkv,G", [(1, 1, 1), (1, 8, 4), (3, 5, 7), (64, 8, 4), (1000, 8, 32)])
 @pytest.mark.parametrize("tiles", [1, 4, 5, 33, 1000, 16384])
 def test_workspace_covers_every_cut(gqa_lib, B, Hkv, G, tiles):
-    # the tiles of all (sequence, head) units in equal runs of at least 4 tiles, one
-    # per CTA, at most 444 CTAs: each CTA writes at most two pieces of G rows
+    # the units (sequence, head), 12 empty places and their tiles each, in equal runs of
+    # at least 4 places, at most 444: each CTA writes at most two pieces of G rows
     got = b.gqa_decode8_workspace_size(B, G * Hkv, Hkv, 64, tiles * 32)
-    ctas = min(444, -(-tiles * B * Hkv // 4))
-    assert got >= (ctas > 1) * (ctas * 2 * G * (64 + 1) * 4 + B * Hkv * 8)
+    ctas = min(444, -(-(tiles + 12) * B * Hkv // 4))
+    assert got >= ctas * 2 * G * (64 + 1) * 4 + B * Hkv * 8
     rng = random.Random(tiles + B)
     for _ in range(20):
         n = [rng.choice([0, 1, tiles, rng.randint(0, tiles)]) for _ in range(min(B, 40)) for _ in range(Hkv)]
-        per = max(4, -(-sum(n) // ctas))
-        assert -(-sum(n) // per) <= ctas
+        total = sum(x + 12 for x in n if x)
+        per = max(4, -(-total // ctas))
+        assert -(-total // per) <= ctas
         at = 0
         begun, carried = [0] * ctas, [0] * ctas
         for x in n:
+            at += 12 if x else 0
             if x and at // per != (at + x - 1) // per:
                 begun[at // per] += 1
                 for c in range(at // per + 1, (at + x - 1) // per + 1):
