@@ -6,7 +6,6 @@ the computation runs in libgqa.so.  Non-OK statuses become exceptions:
 ``NotImplementedError`` for unsupported shapes, ``RuntimeError`` otherwise.
 """
 
-import contextlib
 import math
 from typing import NamedTuple
 
@@ -30,9 +29,16 @@ def _stream(t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+# Handle of the current stream of a device index, without a torch.cuda.Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
 def _need(t, name, dtype, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -314,9 +320,10 @@ def _cache8(cache):
     _need(v, "cache.v", k.dtype, 4)
     _need(ks, "cache.k_scale", torch.float32, 3)
     _need(vs, "cache.v_scale", torch.float32, 3)
-    n_pages, Hkv, page, d = k.shape
+    shape = k.shape
+    n_pages, Hkv, page, d = shape
     n, h, nblk = ks.shape
-    if v.shape != k.shape or vs.shape != ks.shape or n != n_pages or h != Hkv or nblk < 1 or page % nblk:
+    if v.shape != shape or vs.shape != ks.shape or n != n_pages or h != Hkv or nblk < 1 or page % nblk:
         raise ValueError(f"cache shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}, "
                          f"k_scale {tuple(ks.shape)}, v_scale {tuple(vs.shape)}")
     return kind, n_pages, Hkv, page, d, page // nblk
@@ -333,20 +340,26 @@ def _rows_of(table, *vectors):
     return B, M
 
 
-def _on(t, *others):
-    """Checks that the tensors share a device; makes it the current one."""
-    dev = t.device
-    for x in others:
-        if x.device != dev:
-            raise ValueError(f"tensors on {dev} and {x.device}: one device is needed")
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _run(what, tensors, *args):
+    """Calls the C entry point ``what`` with its arguments and the current stream of the
+    tensors' device, which is made the current device for the call."""
+    dev = tensors[0].get_device()
+    for x in tensors:
+        if x.get_device() != dev:
+            raise ValueError(f"tensors on cuda:{dev} and {x.device}: one device is needed")
+    fn = getattr(_b.lib(), what)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
+    if rc != _b.GQA_OK:
+        _check(rc, what)
 
 
 def _scratch(workspace, need, like):
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
     _need(workspace, "workspace", torch.uint8, 1)
     return workspace
 
@@ -365,12 +378,10 @@ def cache8_append_(cache, table, seqlens, k, v, counts=None):
     T = k.shape[1]
     if tuple(k.shape) != (B, T, Hkv, d) or v.shape != k.shape:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [{B}, T, {Hkv}, {d}]")
-    with _on(k, v, table, seqlens, *cache, *(() if counts is None else (counts,))):
-        rc = _b.gqa_cache8_append(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                                  cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(),
-                                  None if counts is None else counts.data_ptr(), k.data_ptr(),
-                                  v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block, _stream(k))
-    _check(rc, "gqa_cache8_append")
+    _run("gqa_cache8_append", (k, v, table, seqlens, *cache, *(() if counts is None else (counts,))),
+         cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
+         table.data_ptr(), seqlens.data_ptr(), None if counts is None else counts.data_ptr(),
+         k.data_ptr(), v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block)
     return cache
 
 
@@ -389,11 +400,9 @@ def cache8_read(cache, table, seqlens, T, out=None):
         _need(t, n, torch.bfloat16, 4)
         if tuple(t.shape) != shape:
             raise ValueError(f"{n} shape {tuple(t.shape)} != {shape}")
-    with _on(table, seqlens, k, v, *cache):
-        rc = _b.gqa_cache8_read(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                                cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(), k.data_ptr(),
-                                v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block, _stream(table))
-    _check(rc, "gqa_cache8_read")
+    _run("gqa_cache8_read", (table, seqlens, k, v, *cache), cache[0].data_ptr(), cache[1].data_ptr(),
+         cache[2].data_ptr(), cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(), k.data_ptr(),
+         v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block)
     return k, v
 
 
@@ -406,11 +415,8 @@ def cache8_copy_(cache, moves):
     _need(moves, "moves", torch.int32, 2)
     if moves.shape[0] < 1 or moves.shape[1] != 3:
         raise ValueError(f"moves must be [1 + cap, 3], got {tuple(moves.shape)}")
-    with _on(moves, *cache):
-        rc = _b.gqa_cache8_copy(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                                cache[3].data_ptr(), moves.data_ptr(), moves.shape[0] - 1, n_pages, Hkv,
-                                page, d, block, _stream(moves))
-    _check(rc, "gqa_cache8_copy")
+    _run("gqa_cache8_copy", (moves, *cache), cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+         cache[3].data_ptr(), moves.data_ptr(), moves.shape[0] - 1, n_pages, Hkv, page, d, block)
     return cache
 
 
@@ -444,15 +450,13 @@ def decode8(q, cache, table, seqlens, scale=None, workspace=None, out=None, wind
         _need(o, "out", torch.bfloat16, 3)
         if o.shape != q.shape:
             raise ValueError(f"out shape {tuple(o.shape)} != q shape {tuple(q.shape)}")
-    workspace = _scratch(workspace, _b.gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page), q)
-    with _on(q, o, table, seqlens, workspace, *cache):
-        rc = _b.gqa_decode8(q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                            cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), kind,
-                            B, Hq, Hkv, d, M, n_pages, page, block, 0 if window is None else int(window),
-                            int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
-                            0.0 if rope_theta is None else float(rope_theta), workspace.data_ptr(),
-                            workspace.numel(), _stream(q))
-    _check(rc, "gqa_decode8")
+    ws = _scratch(workspace, _b.gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page), q)
+    _run("gqa_decode8", (q, o, table, seqlens, ws, *cache), q.data_ptr(), cache[0].data_ptr(),
+         cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), table.data_ptr(),
+         seqlens.data_ptr(), o.data_ptr(), kind, B, Hq, Hkv, d, M, n_pages, page, block,
+         0 if window is None else int(window), int(sinks),
+         1.0 / math.sqrt(d) if scale is None else float(scale),
+         0.0 if rope_theta is None else float(rope_theta), ws.data_ptr(), ws.numel())
     return o
 
 
@@ -474,10 +478,8 @@ def pages_resize_(table, refs, lengths, page, workspace=None):
     page), missing ones taken from the free pages, lowest first.  lengths[b] = 0 frees
     the row.  device_status raises if the pool ran out.  Returns table."""
     B, M, n, ws = _pages(table, refs, workspace, (lengths, "lengths"))
-    with _on(table, refs, lengths, ws):
-        rc = _b.gqa_pages_resize(table.data_ptr(), refs.data_ptr(), lengths.data_ptr(), B, M, n, int(page),
-                                 ws.data_ptr(), ws.numel(), _stream(table))
-    _check(rc, "gqa_pages_resize")
+    _run("gqa_pages_resize", (table, refs, lengths, ws), table.data_ptr(), refs.data_ptr(),
+         lengths.data_ptr(), B, M, n, int(page), ws.data_ptr(), ws.numel())
     return table
 
 
@@ -488,11 +490,9 @@ def pages_fork_(table, refs, seqlens, parents, page, workspace=None):
     [1 + B, 3] to apply with cache8_copy_ to each cache that uses the table."""
     B, M, n, ws = _pages(table, refs, workspace, (seqlens, "seqlens"), (parents, "parents"))
     moves = torch.empty((1 + B, 3), dtype=torch.int32, device=table.device)
-    with _on(table, refs, seqlens, parents, ws):
-        rc = _b.gqa_pages_fork(table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(), parents.data_ptr(),
-                               moves.data_ptr(), B, M, n, int(page), ws.data_ptr(), ws.numel(),
-                               _stream(table))
-    _check(rc, "gqa_pages_fork")
+    _run("gqa_pages_fork", (table, refs, seqlens, parents, ws), table.data_ptr(), refs.data_ptr(),
+         seqlens.data_ptr(), parents.data_ptr(), moves.data_ptr(), B, M, n, int(page), ws.data_ptr(),
+         ws.numel())
     return moves
 
 
@@ -501,10 +501,8 @@ def pages_compact_(table, refs, page, workspace=None):
     [1 + n_pages // 2, 3] to apply with cache8_copy_ to each cache that uses the table."""
     B, M, n, ws = _pages(table, refs, workspace)
     moves = torch.empty((1 + n // 2, 3), dtype=torch.int32, device=table.device)
-    with _on(table, refs, ws):
-        rc = _b.gqa_pages_compact(table.data_ptr(), refs.data_ptr(), moves.data_ptr(), B, M, n, int(page),
-                                  ws.data_ptr(), ws.numel(), _stream(table))
-    _check(rc, "gqa_pages_compact")
+    _run("gqa_pages_compact", (table, refs, ws), table.data_ptr(), refs.data_ptr(), moves.data_ptr(), B, M,
+         n, int(page), ws.data_ptr(), ws.numel())
     return moves
 
 

@@ -63,8 +63,8 @@ struct ApParams {
     Cache8 c;
     const uint4 *k_new, *v_new;
     const int32_t *table, *seqlens, *counts;
-    int B, T, M, n_blk, unit, per_cta;   // n_blk: blocks that T rows can touch
-    long long n_units;
+    int B, T, M, unit, per_cta;
+    uint32_t n_blk, n_units;             // n_blk: blocks that T rows can touch
     int *status;
 };
 
@@ -82,76 +82,77 @@ template <int D, bool kInt8>
 __global__ void __launch_bounds__(512)
 cache8_append_kernel(const ApParams p) {
     constexpr int kC = D / 8;                       // 16-byte columns of an input row
-    __shared__ uint32_t s_max[16];                  // one per warp
-    const int slot = threadIdx.x / p.unit, tid = threadIdx.x % p.unit;
-    const long long u = static_cast<long long>(blockIdx.x) * p.per_cta + slot;
-    const bool real = u < p.n_units;
-    int h = 0, kv = 0, i = 0, b = 0;
-    if (real) {
-        long long x = u;
-        h = static_cast<int>(x % p.c.Hkv);
-        x /= p.c.Hkv;
-        kv = static_cast<int>(x & 1);
-        x >>= 1;
-        i = static_cast<int>(x % p.n_blk);
-        b = static_cast<int>(x / p.n_blk);
-    }
-    const int start = real ? p.seqlens[b] : 0;
-    int count = real ? (p.counts ? p.counts[b] : p.T) : 0;
+    __shared__ uint32_t s_max[2][16];               // one per warp; [1]: finite values only
+    const int slot = threadIdx.x / p.unit, tid = threadIdx.x - slot * p.unit;
+    uint32_t x32 = blockIdx.x * p.per_cta + slot;
+    if (x32 >= p.n_units) return;                   // whole units: they share no barrier
+    uint32_t q = x32 / p.c.Hkv;
+    const int h = x32 - q * p.c.Hkv;
+    const int kv = q & 1;
+    x32 = q >> 1;
+    const int b = x32 / p.n_blk, i = x32 - b * p.n_blk;
+    const int block = p.c.block, start = p.seqlens[b];
+    int count = p.counts ? p.counts[b] : p.T;
     bool bad = start < 0 || start > p.M * p.c.page || count < 0 || count > p.T;
-    if (bad) count = 0;
-    const int block = p.c.block;
     const long long pos0 = static_cast<long long>(start / block + i) * block;
     const int t0 = static_cast<int>(pos0 - start);  // new row of the block's first row (< 0: older rows)
+    if (!bad && t0 >= count) return;
+    if (bad) count = t0;                            // no rows
     const int r0 = max(0, -t0), r1 = min(block, count - t0);
-    bool work = t0 < count;
-    int page = 0, r_page = 0;
-    if (work) {
-        const long long s = pos0 / p.c.page;
-        page = s < p.M ? p.table[static_cast<size_t>(b) * p.M + s] : -1;
-        r_page = static_cast<int>(pos0 % p.c.page);
-        if (page < 0 || page >= p.c.n_pages) {
-            bad = true;
-            work = false;
-        }
-    }
-    if (bad && tid == 0) record_status(p.status, GQA_ERR_INVALID_ARG);
 
     // new rows -> registers; thread tid holds column tid % kC of every step-th row
-    const int col = tid % kC, step = p.unit / kC;
-    const uint4 *src = kv ? p.v_new : p.k_new;
+    const int col = tid % kC, row = tid / kC, step = p.unit / kC;
+    const uint4 *src = (kv ? p.v_new : p.k_new) +
+                       ((static_cast<size_t>(b) * p.T + t0 + row) * p.c.Hkv + h) * kC + col;
+    const size_t stride = static_cast<size_t>(step) * p.c.Hkv * kC;
     uint4 x[kApPasses];
-    uint32_t mx = 0;                                // two bf16 magnitudes
 #pragma unroll
     for (int j = 0; j < kApPasses; ++j) {
-        const int r = tid / kC + j * step;
+        const int r = row + j * step;
         x[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (work && r >= r0 && r < r1)
-            x[j] = src[((static_cast<size_t>(b) * p.T + (t0 + r)) * p.c.Hkv + h) * kC + col];
+        if (r >= r0 && r < r1) x[j] = src[j * stride];
     }
+    int page = -1, r_page = 0;
+    if (!bad) {
+        const long long s = pos0 / p.c.page;
+        r_page = static_cast<int>(pos0 - s * p.c.page);
+        if (s < p.M) page = p.table[static_cast<size_t>(b) * p.M + s];
+    }
+    if (page < 0 || page >= p.c.n_pages) {          // the whole unit
+        if (tid == 0) record_status(p.status, GQA_ERR_INVALID_ARG);
+        return;
+    }
+    const size_t ph = static_cast<size_t>(page) * p.c.Hkv + h;
+    float *scale = (kv ? p.c.v_scale : p.c.k_scale) + ph * (p.c.page / block) + r_page / block;
+    const float s_old = r0 > 0 ? *scale : 0.0f;
+
     auto hmax = [](uint32_t a, uint32_t w) {        // NaN is passed over
         const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
                                          __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
         return *reinterpret_cast<const uint32_t *>(&r);
     };
+    const int warp = threadIdx.x >> 5, unit_warps = p.unit / 32;
+    auto unit_sync = [&]() {
+        if (unit_warps > 1) named_barrier_sync(1 + slot, p.unit);
+        else __syncwarp();
+    };
+    // largest fp32 magnitude of the unit, as bits, from each thread's two bf16 magnitudes
+    auto unit_max = [&](uint32_t v, uint32_t (&s)[16]) {
+        uint32_t m = __reduce_max_sync(0xffffffffu, max(v << 16, v & 0xffff0000u));
+        if (unit_warps > 1) {
+            if ((threadIdx.x & 31) == 0) s[warp] = m;
+            unit_sync();
+            for (int w = 0; w < unit_warps; ++w) m = max(m, s[slot * unit_warps + w]);
+        }
+        return m;
+    };
+    uint32_t mx = 0;
 #pragma unroll
     for (int j = 0; j < kApPasses; ++j)
         mx = hmax(hmax(hmax(hmax(mx, x[j].x), x[j].y), x[j].z), x[j].w);
-    const int warp = threadIdx.x >> 5, unit_warps = p.unit / 32;
-    auto unit_max = [&](uint32_t v) {               // bits of the unit's largest fp32 magnitude
-        uint32_t m = max(v << 16, v & 0xffff0000u);
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (unit_warps == 1) return m;
-        if ((threadIdx.x & 31) == 0) s_max[warp] = m;
-        __syncthreads();
-        for (int w = 0; w < unit_warps; ++w) m = max(m, s_max[slot * unit_warps + w]);
-        __syncthreads();
-        return m;
-    };
-    uint32_t amax = unit_max(mx);
-    // An infinity in the block: the largest finite value counts instead.  All
-    // threads of the CTA take the same branch (unit_max synchronises them).
-    if (__syncthreads_or(amax >= 0x7f800000u)) {
+    uint32_t amax = unit_max(mx, s_max[0]);
+    if (amax >= 0x7f800000u) {
+        // an infinity in the block: the largest finite value counts
         uint32_t fin = 0;
 #pragma unroll
         for (int j = 0; j < kApPasses; ++j) {
@@ -163,41 +164,36 @@ cache8_append_kernel(const ApParams p) {
                 if (hi < 0x7f80u) fin = max(fin, hi);
             }
         }
-        const uint32_t m = unit_max(fin);
-        if (amax >= 0x7f800000u) amax = max(m, 0x10000u);   // not 0: infinities take a scale
+        amax = max(unit_max(fin, s_max[1]), 0x10000u);      // not 0: infinities take a scale
     }
-    if (!work) return;
-    const size_t at = (static_cast<size_t>(page) * p.c.Hkv + h) * (p.c.page / block) + r_page / block;
-    float *scale = (kv ? p.c.v_scale : p.c.k_scale) + at;
-    const float s_old = r0 > 0 ? *scale : 0.0f;
     const float s = fmaxf(scale_for<kInt8>(amax), s_old);
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
     uint2 *dst = reinterpret_cast<uint2 *>(kv ? p.c.v : p.c.k) +
-                 ((static_cast<size_t>(page) * p.c.Hkv + h) * p.c.page + r_page) * kC + col;
+                 (ph * p.c.page + r_page + row) * kC + col;
 #pragma unroll
     for (int j = 0; j < kApPasses; ++j) {
-        const int r = tid / kC + j * step;
-        if (r < r0 && s > s_old) {                  // an older row: to the larger scale
-            uint2 w = dst[r * kC];
+        const int r = row + j * step;
+        uint2 *to = dst + j * step * kC;
+        if (r >= r0 && r < r1) {
+            const float2 a = bf16x2_to_float2(x[j].x), c = bf16x2_to_float2(x[j].y);
+            const float2 e = bf16x2_to_float2(x[j].z), g = bf16x2_to_float2(x[j].w);
+            *to = make_uint2(from_f32x4<kInt8>(a.x * inv, a.y * inv, c.x * inv, c.y * inv),
+                             from_f32x4<kInt8>(e.x * inv, e.y * inv, g.x * inv, g.y * inv));
+        } else if (r < r0 && s > s_old) {           // an older row: to the larger scale
+            const uint2 w = *to;
             float f[4], g[4];
             to_f32x4<kInt8>(w.x, f);
             to_f32x4<kInt8>(w.y, g);
-            w.x = from_f32x4<kInt8>(f[0] * s_old * inv, f[1] * s_old * inv, f[2] * s_old * inv,
-                                    f[3] * s_old * inv);
-            w.y = from_f32x4<kInt8>(g[0] * s_old * inv, g[1] * s_old * inv, g[2] * s_old * inv,
-                                    g[3] * s_old * inv);
-            dst[r * kC] = w;
-        } else if (r >= r0 && r < r1) {
-            const float2 a = bf16x2_to_float2(x[j].x), c = bf16x2_to_float2(x[j].y);
-            const float2 e = bf16x2_to_float2(x[j].z), g = bf16x2_to_float2(x[j].w);
-            dst[r * kC] = make_uint2(
-                from_f32x4<kInt8>(a.x * inv, a.y * inv, c.x * inv, c.y * inv),
-                from_f32x4<kInt8>(e.x * inv, e.y * inv, g.x * inv, g.y * inv));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[e] = f[e] * s_old * inv;
+                g[e] = g[e] * s_old * inv;
+            }
+            *to = make_uint2(from_f32x4<kInt8>(f[0], f[1], f[2], f[3]),
+                             from_f32x4<kInt8>(g[0], g[1], g[2], g[3]));
         }
     }
-    // every thread of the unit has read s_old before it is replaced
-    if (unit_warps > 1) named_barrier_sync(1 + slot, p.unit);
-    else __syncwarp();
+    if (r0 > 0) unit_sync();                        // every thread has read s_old
     if (tid == 0) *scale = s;
 }
 
@@ -365,10 +361,13 @@ extern "C" int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, f
     p.n_blk = (T + block - 2) / block + 1;          // T rows from any row of a block on
     p.unit = (block * d / 64 + 31) / 32 * 32;       // whole warps
     p.per_cta = p.unit >= 128 ? 1 : 128 / p.unit;
-    p.n_units = 2ll * Hkv * p.n_blk * B;
-    const long long ctas = (p.n_units + p.per_cta - 1) / p.per_cta;
-    if (ctas > 0x7fffffffLL) return set_error(GQA_ERR_UNSUPPORTED, "cache8_append grid too large");
-    const unsigned grid = static_cast<unsigned>(ctas), threads = p.unit * p.per_cta;
+    const double units = 2.0 * Hkv * p.n_blk * B;
+    if (units > 2147483647.0)
+        return set_error(GQA_ERR_UNSUPPORTED, "cache8_append: B=%d x T=%d x Hkv=%d rows are too many", B, T,
+                         Hkv);
+    p.n_units = static_cast<uint32_t>(units);
+    const uint32_t ctas = (p.n_units + p.per_cta - 1) / p.per_cta;
+    const unsigned grid = ctas, threads = p.unit * p.per_cta;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (d == 128) {
         if (kind == GQA_INT8) cache8_append_kernel<128, true><<<grid, threads, 0, s>>>(p);
