@@ -51,13 +51,14 @@ int check_table(int B, int M, int page) {
 // ------------------------------------------------------------------ append --
 //
 // Unit: the rows that one call adds to one (sequence, block, K/V head) of K or
-// V, handled by `unit` threads (block * d / 64, in whole warps) that hold the
-// unit's new values in registers (up to 8 16-byte loads each, all in flight):
-// largest magnitude, scale, quantise, store.  Rows of the block from earlier
+// V, handled by `unit` threads (min(block, T) * d / 64, in whole warps) that hold
+// the unit's new values in registers (up to 8 16-byte loads each, all in flight; 4
+// for at most 16 rows of 64): largest magnitude, scale, quantise, store.  Rows of the block from earlier
 // calls are read only when the scale grows.  Units of neighbouring heads share
-// a CTA, so a CTA reads whole runs of the [B, T, Hkv, d] input.
-
-constexpr int kApPasses = 8;
+// a CTA of 256 threads, so a CTA reads whole runs of the [B, T, Hkv, d] input.
+// At most 64 registers a thread keep four such CTAs on an SM (8 prompts of
+// 1024-4096 rows, 8 heads, d = 128, blocks of 64: CTAs of 128 threads 35 us, 256
+// threads with 73 registers 28 us, with 64 registers 25 us, 512 threads 39 us).
 
 struct ApParams {
     Cache8 c;
@@ -78,8 +79,8 @@ __device__ __forceinline__ float scale_for(uint32_t amax_bits) {
     return __uint_as_float(static_cast<uint32_t>(max(x, -126) + 127) << 23);
 }
 
-template <int D, bool kInt8>
-__global__ void __launch_bounds__(512)
+template <int D, bool kInt8, int kPasses>
+__global__ void __launch_bounds__(512, 2)
 cache8_append_kernel(const ApParams p) {
     constexpr int kC = D / 8;                       // 16-byte columns of an input row
     __shared__ uint32_t s_max[2][16];               // one per warp; [1]: finite values only
@@ -100,17 +101,16 @@ cache8_append_kernel(const ApParams p) {
     if (bad) count = t0;                            // no rows
     const int r0 = max(0, -t0), r1 = min(block, count - t0);
 
-    // new rows -> registers; thread tid holds column tid % kC of every step-th row
+    // new rows r0 .. r1 - 1 -> registers; thread tid holds column tid % kC of every step-th
     const int col = tid % kC, row = tid / kC, step = p.unit / kC;
     const uint4 *src = (kv ? p.v_new : p.k_new) +
-                       ((static_cast<size_t>(b) * p.T + t0 + row) * p.c.Hkv + h) * kC + col;
+                       ((static_cast<size_t>(b) * p.T + t0 + r0 + row) * p.c.Hkv + h) * kC + col;
     const size_t stride = static_cast<size_t>(step) * p.c.Hkv * kC;
-    uint4 x[kApPasses];
+    uint4 x[kPasses];
 #pragma unroll
-    for (int j = 0; j < kApPasses; ++j) {
-        const int r = row + j * step;
+    for (int j = 0; j < kPasses; ++j) {
         x[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= r0 && r < r1) x[j] = src[j * stride];
+        if (r0 + row + j * step < r1) x[j] = src[j * stride];
     }
     int page = -1, r_page = 0;
     if (!bad) {
@@ -126,8 +126,8 @@ cache8_append_kernel(const ApParams p) {
     float *scale = (kv ? p.c.v_scale : p.c.k_scale) + ph * (p.c.page / block) + r_page / block;
     const float s_old = r0 > 0 ? *scale : 0.0f;
 
-    auto hmax = [](uint32_t a, uint32_t w) {        // NaN is passed over
-        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+    auto hmax = [](uint32_t a, uint32_t w) {        // NaN if either is
+        const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a),
                                          __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
         return *reinterpret_cast<const uint32_t *>(&r);
     };
@@ -148,39 +148,43 @@ cache8_append_kernel(const ApParams p) {
     };
     uint32_t mx = 0;
 #pragma unroll
-    for (int j = 0; j < kApPasses; ++j)
+    for (int j = 0; j < kPasses; ++j)
         mx = hmax(hmax(hmax(hmax(mx, x[j].x), x[j].y), x[j].z), x[j].w);
     uint32_t amax = unit_max(mx, s_max[0]);
-    if (amax >= 0x7f800000u) {
-        // an infinity in the block: the largest finite value counts
+    const bool special = amax >= 0x7f800000u;       // infinities or NaN among the new values
+    if (special) {
+        // the largest finite value counts; with infinities, at least the smallest one
         uint32_t fin = 0;
 #pragma unroll
-        for (int j = 0; j < kApPasses; ++j) {
+        for (int j = 0; j < kPasses; ++j) {
             const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
-                if (lo < 0x7f80u) fin = max(fin, lo);
-                if (hi < 0x7f80u) fin = max(fin, hi);
+                if (lo <= 0x7f80u) fin = max(fin, lo < 0x7f80u ? lo : 1u);
+                if (hi <= 0x7f80u) fin = max(fin, hi < 0x7f80u ? hi : 1u);
             }
         }
-        amax = max(unit_max(fin, s_max[1]), 0x10000u);      // not 0: infinities take a scale
+        amax = unit_max(fin, s_max[1]);
     }
     const float s = fmaxf(scale_for<kInt8>(amax), s_old);
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-    uint2 *dst = reinterpret_cast<uint2 *>(kv ? p.c.v : p.c.k) +
-                 (ph * p.c.page + r_page + row) * kC + col;
+    uint2 *dst = reinterpret_cast<uint2 *>(kv ? p.c.v : p.c.k) + (ph * p.c.page + r_page) * kC + col;
 #pragma unroll
-    for (int j = 0; j < kApPasses; ++j) {
-        const int r = row + j * step;
-        uint2 *to = dst + j * step * kC;
-        if (r >= r0 && r < r1) {
-            const float2 a = bf16x2_to_float2(x[j].x), c = bf16x2_to_float2(x[j].y);
-            const float2 e = bf16x2_to_float2(x[j].z), g = bf16x2_to_float2(x[j].w);
-            *to = make_uint2(from_f32x4<kInt8>(a.x * inv, a.y * inv, c.x * inv, c.y * inv),
-                             from_f32x4<kInt8>(e.x * inv, e.y * inv, g.x * inv, g.y * inv));
-        } else if (r < r0 && s > s_old) {           // an older row: to the larger scale
-            const uint2 w = *to;
+    for (int j = 0; j < kPasses; ++j) {
+        const int r = r0 + row + j * step;
+        if (r >= r1) continue;
+        const float2 a = bf16x2_to_float2(x[j].x), c = bf16x2_to_float2(x[j].y);
+        const float2 e = bf16x2_to_float2(x[j].z), g = bf16x2_to_float2(x[j].w);
+        dst[r * kC] = special
+                          ? make_uint2(from_f32x4<kInt8>(a.x * inv, a.y * inv, c.x * inv, c.y * inv),
+                                       from_f32x4<kInt8>(e.x * inv, e.y * inv, g.x * inv, g.y * inv))
+                          : make_uint2(from_small_f32x4<kInt8>(a.x * inv, a.y * inv, c.x * inv, c.y * inv),
+                                       from_small_f32x4<kInt8>(e.x * inv, e.y * inv, g.x * inv, g.y * inv));
+    }
+    if (s > s_old)                                  // older rows: to the larger scale
+        for (int r = row; r < r0; r += step) {
+            const uint2 w = dst[r * kC];
             float f[4], g[4];
             to_f32x4<kInt8>(w.x, f);
             to_f32x4<kInt8>(w.y, g);
@@ -189,10 +193,9 @@ cache8_append_kernel(const ApParams p) {
                 f[e] = f[e] * s_old * inv;
                 g[e] = g[e] * s_old * inv;
             }
-            *to = make_uint2(from_f32x4<kInt8>(f[0], f[1], f[2], f[3]),
-                             from_f32x4<kInt8>(g[0], g[1], g[2], g[3]));
+            dst[r * kC] = make_uint2(from_small_f32x4<kInt8>(f[0], f[1], f[2], f[3]),
+                                     from_small_f32x4<kInt8>(g[0], g[1], g[2], g[3]));
         }
-    }
     if (r0 > 0) unit_sync();                        // every thread has read s_old
     if (tid == 0) *scale = s;
 }
@@ -359,8 +362,9 @@ extern "C" int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, f
     p.T = T;
     p.M = M;
     p.n_blk = (T + block - 2) / block + 1;          // T rows from any row of a block on
-    p.unit = (block * d / 64 + 31) / 32 * 32;       // whole warps
-    p.per_cta = p.unit >= 128 ? 1 : 128 / p.unit;
+    const int most = T < block ? T : block;         // new rows of a unit at most
+    p.unit = (most * d / 64 + 31) / 32 * 32;        // whole warps
+    p.per_cta = p.unit >= 256 ? 1 : 256 / p.unit;
     const double units = 2.0 * Hkv * p.n_blk * B;
     if (units > 2147483647.0)
         return set_error(GQA_ERR_UNSUPPORTED, "cache8_append: B=%d x T=%d x Hkv=%d rows are too many", B, T,
@@ -369,12 +373,16 @@ extern "C" int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, f
     const uint32_t ctas = (p.n_units + p.per_cta - 1) / p.per_cta;
     const unsigned grid = ctas, threads = p.unit * p.per_cta;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool int8 = kind == GQA_INT8;
     if (d == 128) {
-        if (kind == GQA_INT8) cache8_append_kernel<128, true><<<grid, threads, 0, s>>>(p);
-        else cache8_append_kernel<128, false><<<grid, threads, 0, s>>>(p);
+        if (int8) cache8_append_kernel<128, true, 8><<<grid, threads, 0, s>>>(p);
+        else cache8_append_kernel<128, false, 8><<<grid, threads, 0, s>>>(p);
+    } else if (most <= 16) {
+        if (int8) cache8_append_kernel<64, true, 4><<<grid, threads, 0, s>>>(p);
+        else cache8_append_kernel<64, false, 4><<<grid, threads, 0, s>>>(p);
     } else {
-        if (kind == GQA_INT8) cache8_append_kernel<64, true><<<grid, threads, 0, s>>>(p);
-        else cache8_append_kernel<64, false><<<grid, threads, 0, s>>>(p);
+        if (int8) cache8_append_kernel<64, true, 8><<<grid, threads, 0, s>>>(p);
+        else cache8_append_kernel<64, false, 8><<<grid, threads, 0, s>>>(p);
     }
     return check_cuda(cudaGetLastError(), "cache8_append_kernel launch");
 }

@@ -78,4 +78,18 @@ __device__ __forceinline__ uint32_t from_f32x4(float a, float b, float c, float 
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// The same for |values| <= 127 (int8): adding 1.5 * 2^23 rounds to an integer, nearest
+// even, and leaves it in the low bits.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t from_small_f32x4(float a, float b, float c, float d) {
+    if constexpr (kInt8) {
+        const uint32_t x = __float_as_uint(__fadd_rn(a, 12582912.0f));
+        const uint32_t y = __float_as_uint(__fadd_rn(b, 12582912.0f));
+        const uint32_t z = __float_as_uint(__fadd_rn(c, 12582912.0f));
+        const uint32_t w = __float_as_uint(__fadd_rn(d, 12582912.0f));
+        return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+    }
+    return from_f32x4<false>(a, b, c, d);
+}
+
 }  // namespace gqa
