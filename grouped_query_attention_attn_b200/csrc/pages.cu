@@ -12,9 +12,12 @@
 // separated by cluster barriers instead of launches, and eight SMs read the
 // table and the counts.  The work is a few bytes per entry; what bounds it is
 // the latency of a phase (a barrier and a dependent load), so the phases are few.
-// Ranks come from one pass of ballots: every warp owns a contiguous range of
-// pages (or entries), publishes its count, and after the barrier all 256 counts
-// are scanned by each CTA for itself.
+// Ranks come from ballots: every warp owns a contiguous range of pages, and one of
+// the table, publishes its counts, and after the barrier all 256 counts are scanned
+// by each CTA for itself.  The entry that needs the k-th page is listed under k, so
+// that the warp that finds the k-th free page can hand it out without a further
+// phase: two barriers a call (three to five before: 16 -> @F@ us for forking 256
+// rows of 128 slots, 7.5 -> @R@ us for taking 5000 pages).
 #include <climits>
 
 #include "device.cuh"
@@ -26,21 +29,20 @@ constexpr int kPgCtas = 8;                   // one portable cluster
 constexpr int kPgThreads = 1024;
 constexpr int kPgWarps = kPgCtas * kPgThreads / 32;
 
+// Everything the cluster's threads wrote before is visible to its threads after
+// (release and acquire at cluster scope, global memory included).
 __device__ __forceinline__ void cluster_barrier() {
-    // release / acquire at cluster scope, after a device-wide fence for the
-    // global writes of the phase
-    __threadfence();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The contiguous range of [0, n) that warp gw owns, in multiples of 32.
+// The contiguous range of [0, n) that warp gw owns, in multiples of `unit`.
 struct PgRange {
-    long long begin, end;
-    __device__ PgRange(long long n, int gw) {
-        const long long seg = (n + 32ll * kPgWarps - 1) / (32ll * kPgWarps) * 32;
-        begin = min(n, seg * gw);
-        end = min(n, begin + seg);
+    int begin, end;
+    __device__ PgRange(int n, int unit, int gw) {
+        const long long seg = (static_cast<long long>(n) + unit * kPgWarps - 1) / (unit * kPgWarps) * unit;
+        begin = static_cast<int>(min(static_cast<long long>(n), seg * gw));
+        end = static_cast<int>(min(static_cast<long long>(n), begin + seg));
     }
 };
 
@@ -66,15 +68,19 @@ __device__ __forceinline__ void pg_scan(const int *counts, int (&out)[kPgWarps +
     __syncthreads();
 }
 
+constexpr int kPgMaxForkRows = 49152;        // 192 KB of shared memory
+constexpr int kPgSlots = 256;                // slots of a piece of a table row, 8 per lane
+
 struct PgParams {
     int32_t *table, *refs, *seqlens;
     const int32_t *lengths, *parents;
     int32_t *moves;
-    int B, M, n_pages, page, cap;
+    int B, M, n_pages, page;
+    int row_pieces;                          // ceil(M / kPgSlots)
     int *status;
     // workspace
     int *count_a, *count_b;                  // one per warp
-    int *list_a, *list_b, *list_c;           // n_pages each
+    int *list_a, *list_b, *list_c;           // lists of pages (n_pages) or table entries (B M)
     int *rows;                               // 4 B
     int *entries;                            // B M
 };
@@ -92,124 +98,134 @@ __device__ __forceinline__ int valid_page(int e, int n_pages, int *status) {
 
 // Free pages of this warp's range, counted.
 __device__ __forceinline__ int count_free(const PgParams &p, int gw, int lane) {
-    const PgRange r(p.n_pages, gw);
+    const PgRange r(p.n_pages, 32, gw);
     int n = 0;
-    for (long long i = r.begin; i < r.end; i += 32) {
+    for (int i = r.begin; i < r.end; i += 32) {
         const bool free = i + lane < r.end && ld(p.refs + i + lane) <= 0;
         n += __popc(__ballot_sync(0xffffffffu, free));
     }
     return n;
 }
 
-// The first `want` free pages of the pool, in order, into list_a, each with one reference.
-__device__ __forceinline__ void take_free(const PgParams &p, int gw, int lane, int rank, int want) {
-    const PgRange r(p.n_pages, gw);
-    for (long long i = r.begin; i < r.end && rank < want; i += 32) {
+// hand(k, page) for the k-th free page of the pool, k < want; rank: of this warp's first.
+template <class F>
+__device__ __forceinline__ void hand_out(const PgParams &p, int gw, int lane, int rank, int want, F hand) {
+    const PgRange r(p.n_pages, 32, gw);
+    for (int i = r.begin; i < r.end && rank < want; i += 32) {
         const bool free = i + lane < r.end && ld(p.refs + i + lane) <= 0;
         const uint32_t m = __ballot_sync(0xffffffffu, free);
         const int k = rank + __popc(m & ((1u << lane) - 1));
         if (free && k < want) {
-            p.list_a[k] = static_cast<int>(i + lane);
             p.refs[i + lane] = 1;
+            hand(k, i + lane);
         }
         rank += __popc(m);
     }
 }
 
 // Pages for the rows' lengths: entries at and past ceil(length / page) are
-// released, missing ones below it get the lowest free pages.
+// released, missing ones below it get the lowest free pages.  list_a: the entry
+// that needs the k-th page.
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 pages_resize_kernel(const PgParams p) {
     __shared__ int need[kPgWarps + 1], avail[kPgWarps + 1], tmp[8];
     const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
-    const long long n = static_cast<long long>(p.B) * p.M;
-    const PgRange r(n, gw);
+    const PgRange r(p.B * p.row_pieces, 1, gw);
+    constexpr int kPer = kPgSlots / 32;
     auto keep = [&](int b) {                  // slots that row b shall hold
         const int L = p.lengths[b];
-        const long long k = L <= 0 ? 0 : (static_cast<long long>(L) + p.page - 1) / p.page;
-        if (L < 0 || k > p.M) record_status(p.status, GQA_ERR_INVALID_ARG);
-        return static_cast<int>(min(k, static_cast<long long>(p.M)));
+        const int k = L <= 0 ? 0 : (L - 1) / p.page + 1;
+        if (lane == 0 && (L < 0 || k > p.M)) record_status(p.status, GQA_ERR_INVALID_ARG);
+        return min(k, p.M);
+    };
+    // piece i of the table: its row, first slot and entries (-1 past the row's end)
+    int e[kPer];
+    auto load = [&](int i, int &b, int &s0) {
+        b = i / p.row_pieces;
+        s0 = (i - b * p.row_pieces) * kPgSlots + lane;
+        const int32_t *row = p.table + static_cast<size_t>(b) * p.M;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) e[x] = s0 + 32 * x < p.M ? row[s0 + 32 * x] : -1;
     };
     int count = 0;
-    for (long long i = r.begin; i < r.end; i += 32) {
-        const long long at = i + lane;
-        bool want = false;
-        if (at < r.end) {
-            const int b = static_cast<int>(at / p.M), s = static_cast<int>(at % p.M);
-            const int raw = p.table[at], e = valid_page(raw, p.n_pages, p.status);
-            if (s < keep(b)) {
-                want = e < 0;
-            } else {
-                if (e >= 0 && atomicSub(p.refs + e, 1) <= 0)
-                    record_status(p.status, GQA_ERR_INVALID_ARG);
-                if (raw != -1) p.table[at] = -1;
-            }
+    for (int i = r.begin; i < r.end; ++i) {
+        int b, s0;
+        load(i, b, s0);
+        const int k = keep(b);
+        int32_t *row = p.table + static_cast<size_t>(b) * p.M;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int s = s0 + 32 * x, v = valid_page(e[x], p.n_pages, p.status);
+            if (s >= k && v >= 0 && atomicSub(p.refs + v, 1) <= 0)
+                record_status(p.status, GQA_ERR_INVALID_ARG);
+            if (e[x] != -1 && (s >= k || v < 0)) row[s] = -1;
+            count += __popc(__ballot_sync(0xffffffffu, s < k && v < 0));
         }
-        count += __popc(__ballot_sync(0xffffffffu, want));
     }
     if (lane == 0) p.count_a[gw] = count;
     cluster_barrier();
     const int free = count_free(p, gw, lane);
     if (lane == 0) p.count_b[gw] = free;
-    cluster_barrier();
     pg_scan(p.count_a, need, tmp);
-    pg_scan(p.count_b, avail, tmp);
-    if (need[kPgWarps] == 0) return;          // the same for every CTA
-    take_free(p, gw, lane, avail[gw], need[kPgWarps]);
-    cluster_barrier();
-    if (need[kPgWarps] > avail[kPgWarps] && gw == 0 && lane == 0)
-        record_status(p.status, GQA_ERR_PAGES);
-    int rank = need[gw];
-    for (long long i = r.begin; i < r.end; i += 32) {
-        const long long at = i + lane;
-        bool want = false;
-        if (at < r.end) {
-            const int e = p.table[at];        // this warp's own range
-            want = static_cast<int>(at % p.M) < keep(static_cast<int>(at / p.M)) &&
-                   (e < 0 || e >= p.n_pages);
+    const int want = need[kPgWarps];
+    if (want == 0) return;                    // the same for every CTA
+    if (count > 0) {
+        int rank = need[gw];
+        for (int i = r.begin; i < r.end; ++i) {
+            int b, s0;
+            load(i, b, s0);                   // this warp's own range
+            const int k = keep(b);
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int s = s0 + 32 * x;
+                const bool w = s < k && e[x] < 0;
+                const uint32_t m = __ballot_sync(0xffffffffu, w);
+                if (w) p.list_a[rank + __popc(m & ((1u << lane) - 1))] = b * p.M + s;
+                rank += __popc(m);
+            }
         }
-        const uint32_t m = __ballot_sync(0xffffffffu, want);
-        const int k = rank + __popc(m & ((1u << lane) - 1));
-        if (want) p.table[at] = k < avail[kPgWarps] ? ld(p.list_a + k) : -1;
-        rank += __popc(m);
     }
+    cluster_barrier();
+    pg_scan(p.count_b, avail, tmp);
+    if (want > avail[kPgWarps] && gw == 0 && lane == 0) record_status(p.status, GQA_ERR_PAGES);
+    hand_out(p, gw, lane, avail[gw], want, [&](int k, int page) { p.table[ld(p.list_a + k)] = page; });
 }
 
-// New row b = old row parents[b].  rows: [heir | length | source page or -1 | rank].
+// New row b = old row parents[b].  rows: [length | source page or -1 | rank of the
+// page it needs | row that needs the k-th page]; shared memory: per parent, the row
+// that goes on in its last page.
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 pages_fork_kernel(const PgParams p) {
+    extern __shared__ int heir[];
     __shared__ int need[kPgWarps + 1], avail[kPgWarps + 1], tmp[8];
     const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
-    const int gt = blockIdx.x * kPgThreads + threadIdx.x;
-    int *heir = p.rows, *length = heir + p.B, *source = length + p.B, *rank_of = source + p.B;
+    int *length = p.rows, *source = length + p.B, *rank_of = source + p.B, *row_of = rank_of + p.B;
     auto parent = [&](int b) {
         const int x = p.parents[b];
         return x >= 0 && x < p.B ? x : -1;
     };
-    for (int b = gt; b < p.B; b += kPgCtas * kPgThreads) {
-        heir[b] = INT_MAX;
-        if (p.parents[b] >= p.B) record_status(p.status, GQA_ERR_INVALID_ARG);
-    }
-    cluster_barrier();
     // the parent's own row goes on in its last page, else its first child does
-    for (int b = gt; b < p.B; b += kPgCtas * kPgThreads) {
+    for (int b = threadIdx.x; b < p.B; b += kPgThreads) heir[b] = INT_MAX;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += kPgThreads) {
         const int x = parent(b);
         if (x >= 0) atomicMin(heir + x, x == b ? -1 : b);
+        if (p.parents[b] >= p.B) record_status(p.status, GQA_ERR_INVALID_ARG);
     }
-    cluster_barrier();
+    __syncthreads();
     // new lengths, and which rows need a page for a copy of the last one
-    const PgRange rb(p.B, gw);
+    const PgRange rb(p.B, 1, gw);
     int count = 0;
-    for (long long i = rb.begin; i < rb.end; i += 32) {
+    for (int i = rb.begin; i < rb.end; i += 32) {
         bool want = false;
         if (i + lane < rb.end) {
-            const int b = static_cast<int>(i + lane), x = parent(b);
+            const int b = i + lane, x = parent(b);
             int L = x >= 0 ? p.seqlens[x] : 0, src = -1;
             if (L < 0 || L > p.M * p.page) {
                 record_status(p.status, GQA_ERR_INVALID_ARG);
                 L = L < 0 ? 0 : p.M * p.page;
             }
-            if (x >= 0 && x != b && ld(heir + x) != b && L % p.page > 0) {
+            if (x >= 0 && x != b && heir[x] != b && L % p.page > 0) {
                 src = valid_page(p.table[static_cast<size_t>(x) * p.M + L / p.page], p.n_pages, p.status);
                 if (src < 0) record_status(p.status, GQA_ERR_INVALID_ARG);
                 want = src >= 0;
@@ -221,63 +237,73 @@ pages_fork_kernel(const PgParams p) {
     }
     if (lane == 0) p.count_a[gw] = count;
     // new rows, and the references that changed rows drop and gain
-    const long long n = static_cast<long long>(p.B) * p.M;
-    for (long long at = gt; at < n; at += kPgCtas * kPgThreads) {
-        const int b = static_cast<int>(at / p.M), s = static_cast<int>(at % p.M), x = parent(b);
-        const int old = p.table[at];
-        int now = old;
-        if (x != b) {
-            now = -1;
-            if (x >= 0) {
-                const int L = max(0, p.seqlens[x]);
-                if (s < L / p.page || ld(heir + x) == b) now = p.table[static_cast<size_t>(x) * p.M + s];
-            }
-            now = valid_page(now, p.n_pages, p.status);
-            const int gone = valid_page(old, p.n_pages, p.status);
-            if (gone != now) {
-                if (gone >= 0) atomicSub(p.refs + gone, 1);
-                if (now >= 0) atomicAdd(p.refs + now, 1);
-            }
+    const PgRange r(p.B * p.row_pieces, 1, gw);
+    constexpr int kPer = kPgSlots / 32;
+    for (int i = r.begin; i < r.end; ++i) {
+        const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane, x = parent(b);
+        if (x == b) continue;
+        const size_t to = static_cast<size_t>(b) * p.M, from = static_cast<size_t>(max(x, 0)) * p.M;
+        const int full = x < 0 ? 0 : (heir[x] == b ? p.M : max(0, p.seqlens[x]) / p.page);
+        int old[kPer], now[kPer];
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const int s = s0 + 32 * y;
+            old[y] = s < p.M ? p.table[to + s] : -1;
+            now[y] = s < p.M && s < full ? p.table[from + s] : -1;
         }
-        p.entries[at] = now;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const int s = s0 + 32 * y;
+            const int on = valid_page(now[y], p.n_pages, p.status), off = valid_page(old[y], p.n_pages, p.status);
+            if (on != off) {
+                if (off >= 0) atomicSub(p.refs + off, 1);
+                if (on >= 0) atomicAdd(p.refs + on, 1);
+            }
+            if (s < p.M) p.entries[to + s] = on;
+        }
     }
     cluster_barrier();
     const int free = count_free(p, gw, lane);
     if (lane == 0) p.count_b[gw] = free;
-    cluster_barrier();
     pg_scan(p.count_a, need, tmp);
-    pg_scan(p.count_b, avail, tmp);
-    const int want = need[kPgWarps], have = min(want, avail[kPgWarps]);
-    take_free(p, gw, lane, avail[gw], want);
+    const int want = need[kPgWarps];
     int rank = need[gw];
-    for (long long i = rb.begin; i < rb.end; i += 32) {
-        const bool w = i + lane < rb.end && source[i + lane] >= 0;      // this warp's own rows
+    for (int i = rb.begin; i < rb.end; i += 32) {
+        const int b = i + lane;
+        const bool w = b < rb.end && source[b] >= 0;             // this warp's own rows
         const uint32_t m = __ballot_sync(0xffffffffu, w);
-        if (i + lane < rb.end) rank_of[i + lane] = w ? rank + __popc(m & ((1u << lane) - 1)) : -1;
+        const int k = rank + __popc(m & ((1u << lane) - 1));
+        if (b < rb.end) rank_of[b] = w ? k : -1;
+        if (w) row_of[k] = b;
         rank += __popc(m);
     }
     cluster_barrier();
-    if (gt == 0) {
+    pg_scan(p.count_b, avail, tmp);
+    const int have = min(want, avail[kPgWarps]);
+    if (gw == 0 && lane == 0) {
         p.moves[0] = have;
         p.moves[1] = p.moves[2] = 0;
         if (want > have) record_status(p.status, GQA_ERR_PAGES);
     }
-    for (long long at = gt; at < n; at += kPgCtas * kPgThreads) {
-        const int b = static_cast<int>(at / p.M), s = static_cast<int>(at % p.M);
-        const int k = ld(rank_of + b), L = ld(length + b);
-        int e = p.entries[at];                // written by this thread
-        if (k >= 0 && s == L / p.page) e = k < have ? ld(p.list_a + k) : -1;
-        p.table[at] = e;
-    }
-    for (int b = gt; b < p.B; b += kPgCtas * kPgThreads) {
-        const int k = ld(rank_of + b), L = ld(length + b);
-        p.seqlens[b] = L;
-        if (k >= 0 && k < have) {
-            p.moves[3 * (1 + k)] = ld(source + b);
-            p.moves[3 * (1 + k) + 1] = ld(p.list_a + k);
-            p.moves[3 * (1 + k) + 2] = L % p.page;
+    hand_out(p, gw, lane, avail[gw], want, [&](int k, int page) {
+        const int b = ld(row_of + k), L = ld(length + b);
+        p.table[static_cast<size_t>(b) * p.M + L / p.page] = page;
+        p.moves[3 * (1 + k)] = ld(source + b);
+        p.moves[3 * (1 + k) + 1] = page;
+        p.moves[3 * (1 + k) + 2] = L % p.page;
+    });
+    for (int i = r.begin; i < r.end; ++i) {
+        const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane;
+        if (parent(b) == b) continue;
+        const int k = ld(rank_of + b), given = k >= 0 && k < have ? ld(length + b) / p.page : -1;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const int s = s0 + 32 * y;
+            if (s < p.M && s != given)        // written by this thread, the given page by another
+                p.table[static_cast<size_t>(b) * p.M + s] = p.entries[static_cast<size_t>(b) * p.M + s];
         }
     }
+    for (int i = rb.begin + lane; i < rb.end; i += 32) p.seqlens[i] = length[i];
 }
 
 // Used pages at and past their number move, in order, to the free pages below it.
@@ -286,8 +312,8 @@ pages_compact_kernel(const PgParams p) {
     __shared__ int used[kPgWarps + 1], tmp[8], s_below;
     const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
     const int gt = blockIdx.x * kPgThreads + threadIdx.x;
-    const PgRange r(p.n_pages, gw);
-    const int mine = static_cast<int>(r.end - r.begin) - count_free(p, gw, lane);
+    const PgRange r(p.n_pages, 32, gw);
+    const int mine = r.end - r.begin - count_free(p, gw, lane);
     if (lane == 0) p.count_a[gw] = mine;
     cluster_barrier();
     pg_scan(p.count_a, used, tmp);
@@ -308,9 +334,9 @@ pages_compact_kernel(const PgParams p) {
     // list_a: free pages below n_used; list_b: used pages past it; list_c: the
     // move of each page past it, -1 for none
     int rank = used[gw];
-    for (long long i = r.begin; i < r.end; i += 32) {
-        const bool in = i + lane < r.end;
-        const int id = static_cast<int>(i + lane);
+    for (int i = r.begin; i < r.end; i += 32) {
+        const int id = i + lane;
+        const bool in = id < r.end;
         const bool u = in && ld(p.refs + id) > 0;
         const uint32_t m = __ballot_sync(0xffffffffu, u);
         const int k = rank + __popc(m & ((1u << lane) - 1));     // used pages before id
@@ -337,27 +363,35 @@ pages_compact_kernel(const PgParams p) {
         p.moves[3 * (1 + k) + 1] = to;
         p.moves[3 * (1 + k) + 2] = p.page;
     }
-    const long long n = static_cast<long long>(p.B) * p.M;
-    for (long long at = gt; at < n; at += kPgCtas * kPgThreads) {
-        const int e = valid_page(p.table[at], p.n_pages, p.status);
-        if (e < n_used) continue;
-        const int k = ld(p.list_c + e);
-        if (k >= 0) p.table[at] = ld(p.list_a + k);
-        else record_status(p.status, GQA_ERR_INVALID_ARG);       // an entry without a reference
+    const PgRange rt(p.B * p.row_pieces, 1, gw);
+    for (int i = rt.begin; i < rt.end; ++i) {
+        const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane;
+        int32_t *row = p.table + static_cast<size_t>(b) * p.M;
+        int e[kPgSlots / 32];
+#pragma unroll
+        for (int x = 0; x < kPgSlots / 32; ++x) e[x] = s0 + 32 * x < p.M ? row[s0 + 32 * x] : -1;
+#pragma unroll
+        for (int x = 0; x < kPgSlots / 32; ++x) {
+            if (valid_page(e[x], p.n_pages, p.status) < n_used) continue;
+            const int k = ld(p.list_c + e[x]);
+            if (k >= 0) row[s0 + 32 * x] = ld(p.list_a + k);
+            else record_status(p.status, GQA_ERR_INVALID_ARG);   // an entry without a reference
+        }
     }
 }
 
 static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Workspace: counts of 2 x 256 warps | 4 ints per row | 3 lists of pages | a copy of the table.
+// Workspace: counts of 2 x 256 warps | 4 ints per row | as many ints as the table has
+// entries (entries, or the list of those that need a page) | 3 lists of pages.
 struct PgWorkspace {
-    size_t off_rows, off_lists, list, off_entries, bytes;
+    size_t off_rows, off_entries, off_lists, list, bytes;
     PgWorkspace(int B, int M, int n_pages) {
         off_rows = 2 * kPgWarps * sizeof(int);
-        off_lists = off_rows + align256(4 * static_cast<size_t>(B) * sizeof(int));
+        off_entries = off_rows + align256(4 * static_cast<size_t>(B) * sizeof(int));
+        off_lists = off_entries + align256(static_cast<size_t>(B) * M * sizeof(int));
         list = align256(static_cast<size_t>(n_pages) * sizeof(int));
-        off_entries = off_lists + 3 * list;
-        bytes = off_entries + align256(static_cast<size_t>(B) * M * sizeof(int));
+        bytes = off_lists + 3 * list;
     }
 };
 
@@ -386,6 +420,7 @@ static int pages_setup(PgParams &p, int32_t *table, int32_t *refs, int B, int M,
     p.count_a = reinterpret_cast<int *>(base);
     p.count_b = p.count_a + kPgWarps;
     p.rows = reinterpret_cast<int *>(base + ws.off_rows);
+    p.row_pieces = (M + kPgSlots - 1) / kPgSlots;
     p.list_a = reinterpret_cast<int *>(base + ws.off_lists);
     p.list_b = reinterpret_cast<int *>(base + ws.off_lists + ws.list);
     p.list_c = reinterpret_cast<int *>(base + ws.off_lists + 2 * ws.list);
@@ -393,11 +428,12 @@ static int pages_setup(PgParams &p, int32_t *table, int32_t *refs, int B, int M,
     return GQA_OK;
 }
 
-static int pages_launch(void (*kern)(PgParams), PgParams &p, gqa_stream_t stream, const char *what) {
+static int pages_launch(void (*kern)(PgParams), PgParams &p, size_t smem, gqa_stream_t stream,
+                        const char *what) {
     if (int rc = require_sm100()) return rc;
     p.status = device_status_ptr();
     if (!p.status) return GQA_ERR_CUDA;
-    kern<<<kPgCtas, kPgThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    kern<<<kPgCtas, kPgThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return check_cuda(cudaGetLastError(), what);
 }
 
@@ -419,7 +455,8 @@ extern "C" int gqa_pages_resize(int32_t *table, int32_t *refs, const int32_t *le
     if (B == 0) return GQA_OK;
     if (int rc = check_ptr(lengths, 4, "lengths")) return rc;
     p.lengths = lengths;
-    return pages_launch(pages_resize_kernel, p, stream, "pages_resize_kernel launch");
+    p.list_a = p.entries;                    // one place per table entry
+    return pages_launch(pages_resize_kernel, p, 0, stream, "pages_resize_kernel launch");
 }
 
 extern "C" int gqa_pages_fork(int32_t *table, int32_t *refs, int32_t *seqlens, const int32_t *parents,
@@ -428,6 +465,8 @@ extern "C" int gqa_pages_fork(int32_t *table, int32_t *refs, int32_t *seqlens, c
     clear_error();
     PgParams p{};
     if (int rc = pages_setup(p, table, refs, B, M, n_pages, page, workspace, workspace_bytes)) return rc;
+    if (B > kPgMaxForkRows)
+        return set_error(GQA_ERR_UNSUPPORTED, "pages_fork: B=%d rows exceed %d", B, kPgMaxForkRows);
     if (int rc = check_ptr(moves, 4, "moves")) return rc;
     if (B > 0) {
         if (int rc = check_ptr(seqlens, 4, "seqlens")) return rc;
@@ -436,7 +475,17 @@ extern "C" int gqa_pages_fork(int32_t *table, int32_t *refs, int32_t *seqlens, c
     p.seqlens = seqlens;
     p.parents = parents;
     p.moves = moves;
-    return pages_launch(pages_fork_kernel, p, stream, "pages_fork_kernel launch");
+    const size_t smem = static_cast<size_t>(B) * sizeof(int);
+    static CtxSlot setup;
+    if (int rc = require_sm100()) return rc;
+    if (int rc = once_per_context(setup, [&](int) {
+            return check_cuda(cudaFuncSetAttribute(pages_fork_kernel,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kPgMaxForkRows * sizeof(int)),
+                              "cudaFuncSetAttribute(pages_fork)");
+        }))
+        return rc;
+    return pages_launch(pages_fork_kernel, p, smem, stream, "pages_fork_kernel launch");
 }
 
 extern "C" int gqa_pages_compact(int32_t *table, int32_t *refs, int32_t *moves, int B, int M,
@@ -447,5 +496,5 @@ extern "C" int gqa_pages_compact(int32_t *table, int32_t *refs, int32_t *moves, 
     if (int rc = pages_setup(p, table, refs, B, M, n_pages, page, workspace, workspace_bytes)) return rc;
     if (int rc = check_ptr(moves, 4, "moves")) return rc;
     p.moves = moves;
-    return pages_launch(pages_compact_kernel, p, stream, "pages_compact_kernel launch");
+    return pages_launch(pages_compact_kernel, p, 0, stream, "pages_compact_kernel launch");
 }
