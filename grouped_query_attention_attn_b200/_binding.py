@@ -4,8 +4,10 @@ names and argument order, argument marshalling only.
 Pointers are passed as Python ints (device addresses, e.g. ``tensor.data_ptr()``
 or 0 for NULL) and the stream as an int (``torch.cuda.Stream.cuda_stream``).
 The functions return the C status code unchanged; ``api.py`` turns codes into
-exceptions.  There is no fallback: if the shared library is missing or fails
-to load, every call raises.
+exceptions (torch_binding.cpp for the calls of the paged 8-bit cache, whose
+kernels are shorter than the checks and the marshalling would be in Python).
+There is no fallback: if the shared library is missing or fails to load, every
+call raises.
 """
 
 import ctypes
@@ -25,6 +27,7 @@ GQA_E4M3 = 0
 GQA_INT8 = 1
 
 _lib = None
+_torch = None
 
 _I = ctypes.c_int
 _P = ctypes.c_void_p
@@ -82,6 +85,22 @@ def lib():
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+def torch_binding():
+    """The extension with the tensor-level calls of the paged 8-bit cache (torch_binding.cpp),
+    bound to the library (raises RuntimeError if either is not built)."""
+    global _torch
+    if _torch is None:
+        handle = lib()
+        try:
+            from . import _torch_binding as ext
+        except ImportError as e:
+            raise RuntimeError("the torch binding is not built: run `python -m "
+                               "grouped_query_attention_attn_b200.build`") from e
+        ext.bind(lambda name: ctypes.cast(getattr(handle, name), ctypes.c_void_p).value)
+        _torch = ext
+    return _torch
 
 
 def gqa_attn_fwd(q, k, v, o, B, Tq, Tkv, Hq, Hkv, d, causal, scale, stream):

@@ -29,16 +29,9 @@ def _stream(t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
-# Handle of the current stream of a device index, without a torch.cuda.Stream object.
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
-    lambda index: torch.cuda.current_stream(index).cuda_stream
-
-
 def _need(t, name, dtype, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
-        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -295,9 +288,6 @@ class Cache8(NamedTuple):
     v_scale: torch.Tensor
 
 
-_KIND8 = {torch.float8_e4m3fn: _b.GQA_E4M3, torch.int8: _b.GQA_INT8}
-
-
 def cache8(n_pages, Hkv, d, page=64, block=64, dtype=torch.float8_e4m3fn, device=None):
     """An empty Cache8 of n_pages pages of ``page`` rows, scales per ``block`` rows."""
     if page < 1 or block < 1 or page % block:
@@ -310,60 +300,6 @@ def cache8(n_pages, Hkv, d, page=64, block=64, dtype=torch.float8_e4m3fn, device
                   torch.zeros(scale, dtype=torch.float32, device=dev))
 
 
-def _cache8(cache):
-    """Checks a Cache8; returns (kind, n_pages, Hkv, page, d, block)."""
-    k, v, ks, vs = cache
-    kind = _KIND8.get(getattr(k, "dtype", None))
-    if kind is None:
-        raise ValueError(f"the cache must be torch.float8_e4m3fn or torch.int8, got {getattr(k, 'dtype', k)}")
-    _need(k, "cache.k", k.dtype, 4)
-    _need(v, "cache.v", k.dtype, 4)
-    _need(ks, "cache.k_scale", torch.float32, 3)
-    _need(vs, "cache.v_scale", torch.float32, 3)
-    shape = k.shape
-    n_pages, Hkv, page, d = shape
-    n, h, nblk = ks.shape
-    if v.shape != shape or vs.shape != ks.shape or n != n_pages or h != Hkv or nblk < 1 or page % nblk:
-        raise ValueError(f"cache shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}, "
-                         f"k_scale {tuple(ks.shape)}, v_scale {tuple(vs.shape)}")
-    return kind, n_pages, Hkv, page, d, page // nblk
-
-
-def _rows_of(table, *vectors):
-    """Checks a page table and int32 [B] vectors given as (tensor, name); returns (B, M)."""
-    _need(table, "table", torch.int32, 2)
-    B, M = table.shape
-    for t, name in vectors:
-        _need(t, name, torch.int32, 1)
-        if t.shape[0] != B:
-            raise ValueError(f"{name} must have {B} entries, one per table row, got {t.shape[0]}")
-    return B, M
-
-
-def _run(what, tensors, *args):
-    """Calls the C entry point ``what`` with its arguments and the current stream of the
-    tensors' device, which is made the current device for the call."""
-    dev = tensors[0].get_device()
-    for x in tensors:
-        if x.get_device() != dev:
-            raise ValueError(f"tensors on cuda:{dev} and {x.device}: one device is needed")
-    fn = getattr(_b.lib(), what)
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev))
-    if rc != _b.GQA_OK:
-        _check(rc, what)
-
-
-def _scratch(workspace, need, like):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    _need(workspace, "workspace", torch.uint8, 1)
-    return workspace
-
-
 def cache8_append_(cache, table, seqlens, k, v, counts=None):
     """Quantise new rows into a Cache8, in place: the first counts[b] (default T) rows
     of bf16 k, v [B, T, Hkv, d] become rows seqlens[b], seqlens[b] + 1, ... of sequence
@@ -371,39 +307,13 @@ def cache8_append_(cache, table, seqlens, k, v, counts=None):
     block is the smallest power of two that covers its rows; rows already in a block
     are requantised when its scale grows.  The page of row seqlens[b] must belong to
     sequence b alone.  Returns cache."""
-    kind, n_pages, Hkv, page, d, block = _cache8(cache)
-    B, M = _rows_of(table, (seqlens, "seqlens"), *(() if counts is None else ((counts, "counts"),)))
-    _need(k, "k", torch.bfloat16, 4)
-    _need(v, "v", torch.bfloat16, 4)
-    T = k.shape[1]
-    if tuple(k.shape) != (B, T, Hkv, d) or v.shape != k.shape:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [{B}, T, {Hkv}, {d}]")
-    _run("gqa_cache8_append", (k, v, table, seqlens, *cache, *(() if counts is None else (counts,))),
-         cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
-         table.data_ptr(), seqlens.data_ptr(), None if counts is None else counts.data_ptr(),
-         k.data_ptr(), v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block)
-    return cache
+    return _b.torch_binding().cache8_append_(cache, table, seqlens, k, v, counts)
 
 
 def cache8_read(cache, table, seqlens, T, out=None):
     """Rows 0 .. T - 1 of every sequence as bf16 (k, v), each [B, T, Hkv, d] (``out``: that
     pair of tensors); rows at and past seqlens[b] are zeros."""
-    kind, n_pages, Hkv, page, d, block = _cache8(cache)
-    B, M = _rows_of(table, (seqlens, "seqlens"))
-    T = int(T)
-    if T < 0:
-        raise ValueError(f"T={T} must be >= 0")
-    shape = (B, T, Hkv, d)
-    k, v = out if out is not None else (torch.empty(shape, dtype=torch.bfloat16, device=table.device),
-                                        torch.empty(shape, dtype=torch.bfloat16, device=table.device))
-    for t, n in ((k, "out[0]"), (v, "out[1]")):
-        _need(t, n, torch.bfloat16, 4)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n} shape {tuple(t.shape)} != {shape}")
-    _run("gqa_cache8_read", (table, seqlens, k, v, *cache), cache[0].data_ptr(), cache[1].data_ptr(),
-         cache[2].data_ptr(), cache[3].data_ptr(), table.data_ptr(), seqlens.data_ptr(), k.data_ptr(),
-         v.data_ptr(), kind, B, T, M, n_pages, Hkv, page, d, block)
-    return k, v
+    return _b.torch_binding().cache8_read(cache, table, seqlens, T, out)
 
 
 def cache8_copy_(cache, moves):
@@ -411,13 +321,7 @@ def cache8_copy_(cache, moves):
     in place: moves[0, 0] moves (src, dst, rows), each replacing the first ``rows`` rows of
     page dst by those of page src.  A page may be the destination of one move only and
     then occur in no other.  Returns cache."""
-    _, n_pages, Hkv, page, d, block = _cache8(cache)
-    _need(moves, "moves", torch.int32, 2)
-    if moves.shape[0] < 1 or moves.shape[1] != 3:
-        raise ValueError(f"moves must be [1 + cap, 3], got {tuple(moves.shape)}")
-    _run("gqa_cache8_copy", (moves, *cache), cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-         cache[3].data_ptr(), moves.data_ptr(), moves.shape[0] - 1, n_pages, Hkv, page, d, block)
-    return cache
+    return _b.torch_binding().cache8_copy_(cache, moves)
 
 
 def decode8_workspace_size(B, Hq, Hkv, d, Lmax):
@@ -435,29 +339,8 @@ def decode8(q, cache, table, seqlens, scale=None, workspace=None, out=None, wind
     max(seqlens[b] - 1, 0)); the cached keys must already be rotated.  ``workspace``: a
     uint8 CUDA tensor of at least decode8_workspace_size(...) bytes (allocated here when
     None)."""
-    kind, n_pages, Hkv, page, d, block = _cache8(cache)
-    B, M = _rows_of(table, (seqlens, "seqlens"))
-    _need(q, "q", torch.bfloat16, 3)
-    Hq = q.shape[1]
-    if tuple(q.shape) != (B, Hq, d):
-        raise ValueError(f"q {tuple(q.shape)} must be [{B}, Hq, {d}]")
-    if window is not None and int(window) < 1:
-        raise ValueError(f"window={window} must be >= 1")
-    if rope_theta is not None and not float(rope_theta) > 0.0:
-        raise ValueError(f"rope_theta={rope_theta} must be > 0")
-    o = torch.empty_like(q) if out is None else out
-    if out is not None:
-        _need(o, "out", torch.bfloat16, 3)
-        if o.shape != q.shape:
-            raise ValueError(f"out shape {tuple(o.shape)} != q shape {tuple(q.shape)}")
-    ws = _scratch(workspace, _b.gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page), q)
-    _run("gqa_decode8", (q, o, table, seqlens, ws, *cache), q.data_ptr(), cache[0].data_ptr(),
-         cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), table.data_ptr(),
-         seqlens.data_ptr(), o.data_ptr(), kind, B, Hq, Hkv, d, M, n_pages, page, block,
-         0 if window is None else int(window), int(sinks),
-         1.0 / math.sqrt(d) if scale is None else float(scale),
-         0.0 if rope_theta is None else float(rope_theta), ws.data_ptr(), ws.numel())
-    return o
+    return _b.torch_binding().decode8(q, cache, table, seqlens, scale, workspace, out, window, sinks,
+                                      rope_theta)
 
 
 def pages_workspace_size(B, M, n_pages):
@@ -465,22 +348,12 @@ def pages_workspace_size(B, M, n_pages):
     return int(_b.gqa_pages_workspace_size(B, M, n_pages))
 
 
-def _pages(table, refs, workspace, *vectors):
-    B, M = _rows_of(table, *vectors)
-    _need(refs, "refs", torch.int32, 1)
-    n = refs.shape[0]
-    return B, M, n, _scratch(workspace, _b.gqa_pages_workspace_size(B, M, n), table)
-
-
 def pages_resize_(table, refs, lengths, page, workspace=None):
     """Give row b of a page table [B, M] exactly the pages that lengths[b] rows need, in
     place: pages past them are released (refs [n_pages] counts the entries that name a
     page), missing ones taken from the free pages, lowest first.  lengths[b] = 0 frees
     the row.  device_status raises if the pool ran out.  Returns table."""
-    B, M, n, ws = _pages(table, refs, workspace, (lengths, "lengths"))
-    _run("gqa_pages_resize", (table, refs, lengths, ws), table.data_ptr(), refs.data_ptr(),
-         lengths.data_ptr(), B, M, n, int(page), ws.data_ptr(), ws.numel())
-    return table
+    return _b.torch_binding().pages_resize_(table, refs, lengths, page, workspace)
 
 
 def pages_fork_(table, refs, seqlens, parents, page, workspace=None):
@@ -488,22 +361,13 @@ def pages_fork_(table, refs, seqlens, parents, page, workspace=None):
     at once and in place, seqlens too: full pages are shared, and every child but one
     gets a page of its own for the last, partly filled one.  Returns the moves
     [1 + B, 3] to apply with cache8_copy_ to each cache that uses the table."""
-    B, M, n, ws = _pages(table, refs, workspace, (seqlens, "seqlens"), (parents, "parents"))
-    moves = torch.empty((1 + B, 3), dtype=torch.int32, device=table.device)
-    _run("gqa_pages_fork", (table, refs, seqlens, parents, ws), table.data_ptr(), refs.data_ptr(),
-         seqlens.data_ptr(), parents.data_ptr(), moves.data_ptr(), B, M, n, int(page), ws.data_ptr(),
-         ws.numel())
-    return moves
+    return _b.torch_binding().pages_fork_(table, refs, seqlens, parents, page, workspace)
 
 
 def pages_compact_(table, refs, page, workspace=None):
     """Move the pages in use to the lowest numbers, in place.  Returns the moves
     [1 + n_pages // 2, 3] to apply with cache8_copy_ to each cache that uses the table."""
-    B, M, n, ws = _pages(table, refs, workspace)
-    moves = torch.empty((1 + n // 2, 3), dtype=torch.int32, device=table.device)
-    _run("gqa_pages_compact", (table, refs, ws), table.data_ptr(), refs.data_ptr(), moves.data_ptr(), B, M,
-         n, int(page), ws.data_ptr(), ws.numel())
-    return moves
+    return _b.torch_binding().pages_compact_(table, refs, page, workspace)
 
 
 def device_status(reset=True):

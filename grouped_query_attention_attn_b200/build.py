@@ -3,8 +3,9 @@
     python -m grouped_query_attention_attn_b200.build [--force] [--verbose]
 
 Each .cu under csrc/ is compiled to an object in _build/ (in parallel), then
-linked into grouped_query_attention_attn_b200/libgqa.so.  Objects are rebuilt
-when their source or any header changed.
+linked into grouped_query_attention_attn_b200/libgqa.so.  csrc/torch_binding.cpp
+becomes the CPython extension _torch_binding.so (g++, torch's headers).  Objects
+are rebuilt when their source or any header changed.
 """
 
 import argparse
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgqa.so")
+TORCH_BINDING = os.path.join(PKG, "_torch_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -48,8 +50,32 @@ def _compile(src, force, verbose, extra):
     return obj, (res.stderr if verbose else "")
 
 
+def _build_torch_binding(force):
+    src = os.path.join(CSRC, "torch_binding.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "gqa.h")))
+    if not force and os.path.exists(TORCH_BINDING) and os.path.getmtime(TORCH_BINDING) >= newest:
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    tmp = TORCH_BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in inc), src, "-o", tmp, f"-L{os.path.join(root, 'lib')}",
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_binding.cpp:\n{res.stderr}")
+    os.replace(tmp, TORCH_BINDING)
+
+
 def build_library(force=False, verbose=False, extra_flags=()):
-    """Compile every CUDA source for sm_100a and link libgqa.so; returns its path."""
+    """Compile every CUDA source for sm_100a and link libgqa.so (returns its path), and
+    build the torch binding."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = _sources()
     extra = list(extra_flags)
@@ -69,6 +95,7 @@ def build_library(force=False, verbose=False, extra_flags=()):
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB)
+    _build_torch_binding(force)
     return LIB
 
 
