@@ -82,6 +82,8 @@ __device__ __forceinline__ float scale_for(uint32_t amax_bits) {
 template <int D, bool kInt8, int kPasses>
 __global__ void __launch_bounds__(512, 2)
 cache8_append_kernel(const ApParams p) {
+    dependents_may_launch();
+    wait_for_stream();
     constexpr int kC = D / 8;                       // 16-byte columns of an input row
     __shared__ uint32_t s_max[2][16];               // one per warp; [1]: finite values only
     const int slot = threadIdx.x / p.unit, tid = threadIdx.x - slot * p.unit;
@@ -219,6 +221,8 @@ struct RdParams {
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(256)
 cache8_read_kernel(const RdParams p) {
+    dependents_may_launch();
+    wait_for_stream();
     constexpr int kC = D / 8, kRows = 32 / kC, kN = kC8Rows / kRows;   // 8 bytes in, 16 out per lane
     const long long u = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     if (u >= p.n_warps) return;
@@ -287,6 +291,8 @@ constexpr int kCpThreads = 128, kCpBatch = 4;
 
 __global__ void __launch_bounds__(kCpThreads)
 cache8_copy_kernel(const CpParams p) {
+    dependents_may_launch();
+    wait_for_stream();
     int n = p.moves[0];
     if (n < 0 || n > p.cap) {
         if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, GQA_ERR_INVALID_ARG);
@@ -374,17 +380,10 @@ extern "C" int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, f
     const unsigned grid = ctas, threads = p.unit * p.per_cta;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool int8 = kind == GQA_INT8;
-    if (d == 128) {
-        if (int8) cache8_append_kernel<128, true, 8><<<grid, threads, 0, s>>>(p);
-        else cache8_append_kernel<128, false, 8><<<grid, threads, 0, s>>>(p);
-    } else if (most <= 16) {
-        if (int8) cache8_append_kernel<64, true, 4><<<grid, threads, 0, s>>>(p);
-        else cache8_append_kernel<64, false, 4><<<grid, threads, 0, s>>>(p);
-    } else {
-        if (int8) cache8_append_kernel<64, true, 8><<<grid, threads, 0, s>>>(p);
-        else cache8_append_kernel<64, false, 8><<<grid, threads, 0, s>>>(p);
-    }
-    return check_cuda(cudaGetLastError(), "cache8_append_kernel launch");
+    auto kern = d == 128     ? (int8 ? cache8_append_kernel<128, true, 8> : cache8_append_kernel<128, false, 8>)
+                : most <= 16 ? (int8 ? cache8_append_kernel<64, true, 4> : cache8_append_kernel<64, false, 4>)
+                             : (int8 ? cache8_append_kernel<64, true, 8> : cache8_append_kernel<64, false, 8>);
+    return launch_dependent(kern, grid, threads, 0, s, "cache8_append_kernel launch", p);
 }
 
 extern "C" int gqa_cache8_read(const void *k_cache, const void *v_cache, const float *k_scale,
@@ -420,14 +419,10 @@ extern "C" int gqa_cache8_read(const void *k_cache, const void *v_cache, const f
     if (ctas > 0x7fffffffLL) return set_error(GQA_ERR_UNSUPPORTED, "cache8_read grid too large");
     const unsigned grid = static_cast<unsigned>(ctas);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 128) {
-        if (kind == GQA_INT8) cache8_read_kernel<128, true><<<grid, 256, 0, s>>>(p);
-        else cache8_read_kernel<128, false><<<grid, 256, 0, s>>>(p);
-    } else {
-        if (kind == GQA_INT8) cache8_read_kernel<64, true><<<grid, 256, 0, s>>>(p);
-        else cache8_read_kernel<64, false><<<grid, 256, 0, s>>>(p);
-    }
-    return check_cuda(cudaGetLastError(), "cache8_read_kernel launch");
+    const bool int8 = kind == GQA_INT8;
+    auto kern = d == 128 ? (int8 ? cache8_read_kernel<128, true> : cache8_read_kernel<128, false>)
+                         : (int8 ? cache8_read_kernel<64, true> : cache8_read_kernel<64, false>);
+    return launch_dependent(kern, grid, 256, 0, s, "cache8_read_kernel launch", p);
 }
 
 extern "C" int gqa_cache8_copy(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
@@ -448,7 +443,6 @@ extern "C" int gqa_cache8_copy(void *k_cache, void *v_cache, float *k_scale, flo
     int n_sm = 0;
     if (int rc = sm_count(&n_sm)) return rc;
     const long long units = 2ll * cap * Hkv, full = 16ll * n_sm;
-    cache8_copy_kernel<<<static_cast<unsigned>(units < full ? units : full), kCpThreads, 0,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return check_cuda(cudaGetLastError(), "cache8_copy_kernel launch");
+    return launch_dependent(cache8_copy_kernel, static_cast<unsigned>(units < full ? units : full), kCpThreads,
+                            0, reinterpret_cast<cudaStream_t>(stream), "cache8_copy_kernel launch", p);
 }

@@ -15,6 +15,33 @@
 
 namespace gqa {
 
+// Programmatic dependent launch.  These kernels are short and follow one another (fork,
+// copy, append, decode), so each is launched while its predecessor still runs and
+// waits, before it touches memory, for that kernel to be complete: the launch costs
+// then overlap.  Every thread calls dependents_may_launch() and wait_for_stream() first.
+__device__ __forceinline__ void dependents_may_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class Kernel, class... Args>
+int launch_dependent(Kernel kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                     const char *what, const Args &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, args...), what);
+}
+
 struct Cache8 {
     void *k, *v;
     float *k_scale, *v_scale;

@@ -197,6 +197,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         tma_prefetch_desc(&tm_v);
     }
     __syncwarp();
+    dependents_may_launch();
+    wait_for_stream();
     // places that each unit of sequence b takes in the line of tiles: kD8Begin empty
     // ones, then its tiles
     auto places_of = [&](int b) {
@@ -819,8 +821,8 @@ static int launch_decode8_kernel(const CUtensorMap &tk, const CUtensorMap &tv, c
     int n_sm = 0;
     if (int rc = sm_count(&n_sm)) return rc;
     const int most = min(kD8MaxCtas, n_sm * d8_ctas_per_sm<NT>());     // all resident at once
-    kern<<<d8_grid(p.B, p.Hkv, tiles, most), kD8Threads, smem, stream>>>(tk, tv, p);
-    return check_cuda(cudaGetLastError(), "decode8_kernel launch");
+    return launch_dependent(kern, d8_grid(p.B, p.Hkv, tiles, most), kD8Threads, smem, stream,
+                            "decode8_kernel launch", tk, tv, p);
 }
 
 template <int D, int NT>

@@ -20,8 +20,7 @@
 // rows of 128 slots, 7.5 -> @R@ us for taking 5000 pages).
 #include <climits>
 
-#include "device.cuh"
-#include "internal.h"
+#include "cache8.cuh"
 
 namespace gqa {
 
@@ -128,6 +127,8 @@ __device__ __forceinline__ void hand_out(const PgParams &p, int gw, int lane, in
 // that needs the k-th page.
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 pages_resize_kernel(const PgParams p) {
+    dependents_may_launch();
+    wait_for_stream();
     __shared__ int need[kPgWarps + 1], avail[kPgWarps + 1], tmp[8];
     const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
     const PgRange r(p.B * p.row_pieces, 1, gw);
@@ -196,6 +197,8 @@ pages_resize_kernel(const PgParams p) {
 // that goes on in its last page.
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 pages_fork_kernel(const PgParams p) {
+    dependents_may_launch();
+    wait_for_stream();
     extern __shared__ int heir[];
     __shared__ int need[kPgWarps + 1], avail[kPgWarps + 1], tmp[8];
     const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
@@ -309,6 +312,8 @@ pages_fork_kernel(const PgParams p) {
 // Used pages at and past their number move, in order, to the free pages below it.
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 pages_compact_kernel(const PgParams p) {
+    dependents_may_launch();
+    wait_for_stream();
     __shared__ int used[kPgWarps + 1], tmp[8], s_below;
     const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
     const int gt = blockIdx.x * kPgThreads + threadIdx.x;
@@ -433,8 +438,7 @@ static int pages_launch(void (*kern)(PgParams), PgParams &p, size_t smem, gqa_st
     if (int rc = require_sm100()) return rc;
     p.status = device_status_ptr();
     if (!p.status) return GQA_ERR_CUDA;
-    kern<<<kPgCtas, kPgThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return check_cuda(cudaGetLastError(), what);
+    return launch_dependent(kern, kPgCtas, kPgThreads, smem, reinterpret_cast<cudaStream_t>(stream), what, p);
 }
 
 }  // namespace gqa
