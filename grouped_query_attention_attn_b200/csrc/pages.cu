@@ -12,12 +12,15 @@
 // separated by cluster barriers instead of launches, and eight SMs read the
 // table and the counts.  The work is a few bytes per entry; what bounds it is
 // the latency of a phase (a barrier and a dependent load), so the phases are few.
+// Rows, table and pages are spread over the warps from three different starts, so that
+// for small sizes each warp has one of them and their loads run side by side.
 // Ranks come from ballots: every warp owns a contiguous range of pages, and one of
 // the table, publishes its counts, and after the barrier all 256 counts are scanned
 // by each CTA for itself.  The entry that needs the k-th page is listed under k, so
 // that the warp that finds the k-th free page can hand it out without a further
-// phase: two barriers a call (three to five before: 16 -> @F@ us for forking 256
-// rows of 128 slots, 7.5 -> @R@ us for taking 5000 pages).
+// phase: two barriers a call.  Forking 256 rows of 128 slots took 16.0 us with five
+// barriers, 11.0 us with two and 8.6 us with the loads side by side, 4 rows 10.9, 9.4
+// and 6.2 us; freeing and taking the 4600 pages of 96 rows 15.1, 12.6 and 10.4 us.
 #include <climits>
 
 #include "cache8.cuh"
@@ -45,12 +48,15 @@ struct PgRange {
     }
 };
 
-// Exclusive prefix sums of 256 counts published in global memory; total in out[256].
-__device__ __forceinline__ void pg_scan(const int *counts, int (&out)[kPgWarps + 1], int (&tmp)[8]) {
+// Exclusive prefix sums of the 256 counts that the warps published, total in out[256];
+// mine: count number threadIdx.x, loaded by the caller as early as it can.
+__device__ __forceinline__ int published(const int *counts) {
+    return threadIdx.x < kPgWarps ? __ldcg(counts + threadIdx.x) : 0;
+}
+__device__ __forceinline__ void pg_scan(int mine, int (&out)[kPgWarps + 1], int (&tmp)[8]) {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    int v = 0, x = 0;
+    int x = mine;
     if (t < kPgWarps) {
-        v = x = __ldcg(counts + t);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -60,11 +66,19 @@ __device__ __forceinline__ void pg_scan(const int *counts, int (&out)[kPgWarps +
     }
     __syncthreads();
     if (t < kPgWarps) {
-        for (int i = 0; i < w; ++i) x += tmp[i];
-        out[t] = x - v;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < w) x += tmp[i];
+        out[t] = x - mine;
         if (t == kPgWarps - 1) out[kPgWarps] = x;
     }
     __syncthreads();
+}
+
+// Number of this warp among the cluster's, from the k-th of three starts.
+__device__ __forceinline__ int pg_warp(int k) {
+    const int w = static_cast<int>(threadIdx.x >> 5) * kPgCtas + blockIdx.x;
+    return (w + k * (kPgWarps / 3)) % kPgWarps;
 }
 
 constexpr int kPgMaxForkRows = 49152;        // 192 KB of shared memory
@@ -80,7 +94,7 @@ struct PgParams {
     // workspace
     int *count_a, *count_b;                  // one per warp
     int *list_a, *list_b, *list_c;           // lists of pages (n_pages) or table entries (B M)
-    int *rows;                               // 4 B
+    int *rows;                               // 8 B
     int *entries;                            // B M
 };
 
@@ -95,32 +109,37 @@ __device__ __forceinline__ int valid_page(int e, int n_pages, int *status) {
     return e < 0 ? -1 : e;
 }
 
-// Free pages of this warp's range, counted.
-__device__ __forceinline__ int count_free(const PgParams &p, int gw, int lane) {
-    const PgRange r(p.n_pages, 32, gw);
-    int n = 0;
-    for (int i = r.begin; i < r.end; i += 32) {
-        const bool free = i + lane < r.end && ld(p.refs + i + lane) <= 0;
-        n += __popc(__ballot_sync(0xffffffffu, free));
-    }
-    return n;
-}
+// Free pages of a warp's range: counted, then handed out.
+struct FreePages {
+    PgRange r;
+    int warp, count = 0;
+    uint32_t first = 0;                       // the first 32 pages' free ones
 
-// hand(k, page) for the k-th free page of the pool, k < want; rank: of this warp's first.
-template <class F>
-__device__ __forceinline__ void hand_out(const PgParams &p, int gw, int lane, int rank, int want, F hand) {
-    const PgRange r(p.n_pages, 32, gw);
-    for (int i = r.begin; i < r.end && rank < want; i += 32) {
-        const bool free = i + lane < r.end && ld(p.refs + i + lane) <= 0;
-        const uint32_t m = __ballot_sync(0xffffffffu, free);
-        const int k = rank + __popc(m & ((1u << lane) - 1));
-        if (free && k < want) {
-            p.refs[i + lane] = 1;
-            hand(k, i + lane);
+    __device__ FreePages(const PgParams &p) : r(p.n_pages, 32, pg_warp(2)), warp(pg_warp(2)) {
+        const int lane = threadIdx.x & 31;
+        for (int i = r.begin; i < r.end; i += 32) {
+            const uint32_t m = __ballot_sync(0xffffffffu, i + lane < r.end && ld(p.refs + i + lane) <= 0);
+            if (i == r.begin) first = m;
+            count += __popc(m);
         }
-        rank += __popc(m);
     }
-}
+    // hand(k, page) for the pool's k-th free page, k < want; rank: of this range's first
+    template <class F>
+    __device__ void hand_out(const PgParams &p, int rank, int want, F hand) const {
+        const int lane = threadIdx.x & 31;
+        for (int i = r.begin; i < r.end && rank < want; i += 32) {
+            const uint32_t m = i == r.begin ? first
+                                            : __ballot_sync(0xffffffffu, i + lane < r.end &&
+                                                                             ld(p.refs + i + lane) <= 0);
+            const int k = rank + __popc(m & ((1u << lane) - 1));
+            if ((m >> lane & 1) && k < want) {
+                p.refs[i + lane] = 1;
+                hand(k, i + lane);
+            }
+            rank += __popc(m);
+        }
+    }
+};
 
 // Pages for the rows' lengths: entries at and past ceil(length / page) are
 // released, missing ones below it get the lowest free pages.  list_a: the entry
@@ -130,7 +149,7 @@ pages_resize_kernel(const PgParams p) {
     dependents_may_launch();
     wait_for_stream();
     __shared__ int need[kPgWarps + 1], avail[kPgWarps + 1], tmp[8];
-    const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31, gw = pg_warp(0);
     const PgRange r(p.B * p.row_pieces, 1, gw);
     constexpr int kPer = kPgSlots / 32;
     auto keep = [&](int b) {                  // slots that row b shall hold
@@ -165,9 +184,10 @@ pages_resize_kernel(const PgParams p) {
     }
     if (lane == 0) p.count_a[gw] = count;
     cluster_barrier();
-    const int free = count_free(p, gw, lane);
-    if (lane == 0) p.count_b[gw] = free;
-    pg_scan(p.count_a, need, tmp);
+    const int needed = published(p.count_a);
+    const FreePages pages(p);
+    if (lane == 0) p.count_b[pages.warp] = pages.count;
+    pg_scan(needed, need, tmp);
     const int want = need[kPgWarps];
     if (want == 0) return;                    // the same for every CTA
     if (count > 0) {
@@ -187,22 +207,21 @@ pages_resize_kernel(const PgParams p) {
         }
     }
     cluster_barrier();
-    pg_scan(p.count_b, avail, tmp);
+    pg_scan(published(p.count_b), avail, tmp);
     if (want > avail[kPgWarps] && gw == 0 && lane == 0) record_status(p.status, GQA_ERR_PAGES);
-    hand_out(p, gw, lane, avail[gw], want, [&](int k, int page) { p.table[ld(p.list_a + k)] = page; });
+    pages.hand_out(p, avail[pages.warp], want, [&](int k, int page) { p.table[ld(p.list_a + k)] = page; });
 }
 
-// New row b = old row parents[b].  rows: [length | source page or -1 | rank of the
-// page it needs | row that needs the k-th page]; shared memory: per parent, the row
-// that goes on in its last page.
+// New row b = old row parents[b].  needs: {row, its source page, its length, -} of the
+// row that needs the k-th page; shared memory: per parent, the row that goes on in its
+// last page.
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 pages_fork_kernel(const PgParams p) {
     dependents_may_launch();
     wait_for_stream();
     extern __shared__ int heir[];
     __shared__ int need[kPgWarps + 1], avail[kPgWarps + 1], tmp[8];
-    const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
-    int *length = p.rows, *source = length + p.B, *rank_of = source + p.B, *row_of = rank_of + p.B;
+    const int lane = threadIdx.x & 31;
     auto parent = [&](int b) {
         const int x = p.parents[b];
         return x >= 0 && x < p.B ? x : -1;
@@ -216,14 +235,18 @@ pages_fork_kernel(const PgParams p) {
         if (p.parents[b] >= p.B) record_status(p.status, GQA_ERR_INVALID_ARG);
     }
     __syncthreads();
+    auto full_slots = [&](int b, int x) {     // slots that row b takes over from row x
+        return x < 0 ? 0 : (heir[x] == b ? p.M : max(0, p.seqlens[x]) / p.page);
+    };
     // new lengths, and which rows need a page for a copy of the last one
-    const PgRange rb(p.B, 1, gw);
-    int count = 0;
+    const int row_warp = pg_warp(1);
+    const PgRange rb(p.B, 1, row_warp);
+    int count = 0, src = -1, L = 0;           // of this lane's last row
     for (int i = rb.begin; i < rb.end; i += 32) {
-        bool want = false;
+        src = -1;
         if (i + lane < rb.end) {
             const int b = i + lane, x = parent(b);
-            int L = x >= 0 ? p.seqlens[x] : 0, src = -1;
+            L = x >= 0 ? p.seqlens[x] : 0;
             if (L < 0 || L > p.M * p.page) {
                 record_status(p.status, GQA_ERR_INVALID_ARG);
                 L = L < 0 ? 0 : p.M * p.page;
@@ -231,23 +254,23 @@ pages_fork_kernel(const PgParams p) {
             if (x >= 0 && x != b && heir[x] != b && L % p.page > 0) {
                 src = valid_page(p.table[static_cast<size_t>(x) * p.M + L / p.page], p.n_pages, p.status);
                 if (src < 0) record_status(p.status, GQA_ERR_INVALID_ARG);
-                want = src >= 0;
             }
-            length[b] = L;
-            source[b] = src;
+            p.rows[b] = L;
+            p.rows[p.B + b] = src;
         }
-        count += __popc(__ballot_sync(0xffffffffu, want));
+        count += __popc(__ballot_sync(0xffffffffu, src >= 0));
     }
-    if (lane == 0) p.count_a[gw] = count;
+    if (lane == 0) p.count_a[row_warp] = count;
     // new rows, and the references that changed rows drop and gain
-    const PgRange r(p.B * p.row_pieces, 1, gw);
+    const PgRange r(p.B * p.row_pieces, 1, pg_warp(0));
     constexpr int kPer = kPgSlots / 32;
+    int now[kPer] = {};                       // of the last piece
     for (int i = r.begin; i < r.end; ++i) {
         const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane, x = parent(b);
         if (x == b) continue;
         const size_t to = static_cast<size_t>(b) * p.M, from = static_cast<size_t>(max(x, 0)) * p.M;
-        const int full = x < 0 ? 0 : (heir[x] == b ? p.M : max(0, p.seqlens[x]) / p.page);
-        int old[kPer], now[kPer];
+        const int full = full_slots(b, x);
+        int old[kPer];
 #pragma unroll
         for (int y = 0; y < kPer; ++y) {
             const int s = s0 + 32 * y;
@@ -256,57 +279,64 @@ pages_fork_kernel(const PgParams p) {
         }
 #pragma unroll
         for (int y = 0; y < kPer; ++y) {
-            const int s = s0 + 32 * y;
-            const int on = valid_page(now[y], p.n_pages, p.status), off = valid_page(old[y], p.n_pages, p.status);
-            if (on != off) {
+            const int s = s0 + 32 * y, off = valid_page(old[y], p.n_pages, p.status);
+            now[y] = valid_page(now[y], p.n_pages, p.status);
+            if (now[y] != off) {
                 if (off >= 0) atomicSub(p.refs + off, 1);
-                if (on >= 0) atomicAdd(p.refs + on, 1);
+                if (now[y] >= 0) atomicAdd(p.refs + now[y], 1);
             }
-            if (s < p.M) p.entries[to + s] = on;
+            if (s < p.M && i + 1 < r.end) p.entries[to + s] = now[y];
         }
     }
     cluster_barrier();
-    const int free = count_free(p, gw, lane);
-    if (lane == 0) p.count_b[gw] = free;
-    pg_scan(p.count_a, need, tmp);
+    const int needed = published(p.count_a);
+    const FreePages pages(p);
+    if (lane == 0) p.count_b[pages.warp] = pages.count;
+    pg_scan(needed, need, tmp);
     const int want = need[kPgWarps];
-    int rank = need[gw];
-    for (int i = rb.begin; i < rb.end; i += 32) {
-        const int b = i + lane;
-        const bool w = b < rb.end && source[b] >= 0;             // this warp's own rows
-        const uint32_t m = __ballot_sync(0xffffffffu, w);
-        const int k = rank + __popc(m & ((1u << lane) - 1));
-        if (b < rb.end) rank_of[b] = w ? k : -1;
-        if (w) row_of[k] = b;
-        rank += __popc(m);
+    int4 *needs = reinterpret_cast<int4 *>(p.rows + 4 * static_cast<size_t>(p.B));
+    if (count > 0) {
+        int rank = need[row_warp];
+        for (int i = rb.begin; i < rb.end; i += 32) {
+            const int b = i + lane;
+            if (rb.end - rb.begin > 32) {     // this warp's own rows
+                src = b < rb.end ? p.rows[p.B + b] : -1;
+                L = b < rb.end ? p.rows[b] : 0;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, src >= 0);
+            if (src >= 0) needs[rank + __popc(m & ((1u << lane) - 1))] = make_int4(b, src, L, 0);
+            rank += __popc(m);
+        }
+    }
+    // rows without a page of their own to come: the table (every old row has been read)
+    for (int i = r.begin; i < r.end; ++i) {
+        const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane, x = parent(b);
+        if (x == b) continue;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const int s = s0 + 32 * y;
+            if (s < p.M)
+                p.table[static_cast<size_t>(b) * p.M + s] =
+                    i + 1 < r.end ? p.entries[static_cast<size_t>(b) * p.M + s] : now[y];
+        }
     }
     cluster_barrier();
-    pg_scan(p.count_b, avail, tmp);
+    pg_scan(published(p.count_b), avail, tmp);
     const int have = min(want, avail[kPgWarps]);
-    if (gw == 0 && lane == 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.moves[0] = have;
         p.moves[1] = p.moves[2] = 0;
         if (want > have) record_status(p.status, GQA_ERR_PAGES);
     }
-    hand_out(p, gw, lane, avail[gw], want, [&](int k, int page) {
-        const int b = ld(row_of + k), L = ld(length + b);
-        p.table[static_cast<size_t>(b) * p.M + L / p.page] = page;
-        p.moves[3 * (1 + k)] = ld(source + b);
+    pages.hand_out(p, avail[pages.warp], want, [&](int k, int page) {
+        const int4 n = __ldcg(needs + k);
+        p.table[static_cast<size_t>(n.x) * p.M + n.z / p.page] = page;
+        p.moves[3 * (1 + k)] = n.y;
         p.moves[3 * (1 + k) + 1] = page;
-        p.moves[3 * (1 + k) + 2] = L % p.page;
+        p.moves[3 * (1 + k) + 2] = n.z % p.page;
     });
-    for (int i = r.begin; i < r.end; ++i) {
-        const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane;
-        if (parent(b) == b) continue;
-        const int k = ld(rank_of + b), given = k >= 0 && k < have ? ld(length + b) / p.page : -1;
-#pragma unroll
-        for (int y = 0; y < kPer; ++y) {
-            const int s = s0 + 32 * y;
-            if (s < p.M && s != given)        // written by this thread, the given page by another
-                p.table[static_cast<size_t>(b) * p.M + s] = p.entries[static_cast<size_t>(b) * p.M + s];
-        }
-    }
-    for (int i = rb.begin + lane; i < rb.end; i += 32) p.seqlens[i] = length[i];
+    for (int i = rb.begin + lane; i < rb.end; i += 32)
+        p.seqlens[i] = rb.end - rb.begin > 32 ? p.rows[i] : L;
 }
 
 // Used pages at and past their number move, in order, to the free pages below it.
@@ -315,13 +345,13 @@ pages_compact_kernel(const PgParams p) {
     dependents_may_launch();
     wait_for_stream();
     __shared__ int used[kPgWarps + 1], tmp[8], s_below;
-    const int lane = threadIdx.x & 31, gw = (blockIdx.x * kPgThreads + threadIdx.x) >> 5;
-    const int gt = blockIdx.x * kPgThreads + threadIdx.x;
-    const PgRange r(p.n_pages, 32, gw);
-    const int mine = r.end - r.begin - count_free(p, gw, lane);
-    if (lane == 0) p.count_a[gw] = mine;
+    const int lane = threadIdx.x & 31;
+    const int gt = threadIdx.x * kPgCtas + blockIdx.x;
+    const FreePages pages(p);
+    const PgRange r = pages.r;
+    if (lane == 0) p.count_a[pages.warp] = r.end - r.begin - pages.count;
     cluster_barrier();
-    pg_scan(p.count_a, used, tmp);
+    pg_scan(published(p.count_a), used, tmp);
     const int n_used = used[kPgWarps];
     // used pages below n_used: whole ranges, and the part of the one that n_used cuts
     if (threadIdx.x < 32) {
@@ -338,11 +368,11 @@ pages_compact_kernel(const PgParams p) {
     const int below = s_below, n_moves = n_used - below;
     // list_a: free pages below n_used; list_b: used pages past it; list_c: the
     // move of each page past it, -1 for none
-    int rank = used[gw];
+    int rank = used[pages.warp];
     for (int i = r.begin; i < r.end; i += 32) {
         const int id = i + lane;
         const bool in = id < r.end;
-        const bool u = in && ld(p.refs + id) > 0;
+        const bool u = in && (i == r.begin ? !(pages.first >> lane & 1) : ld(p.refs + id) > 0);
         const uint32_t m = __ballot_sync(0xffffffffu, u);
         const int k = rank + __popc(m & ((1u << lane) - 1));     // used pages before id
         if (in) {
@@ -368,7 +398,7 @@ pages_compact_kernel(const PgParams p) {
         p.moves[3 * (1 + k) + 1] = to;
         p.moves[3 * (1 + k) + 2] = p.page;
     }
-    const PgRange rt(p.B * p.row_pieces, 1, gw);
+    const PgRange rt(p.B * p.row_pieces, 1, pg_warp(0));
     for (int i = rt.begin; i < rt.end; ++i) {
         const int b = i / p.row_pieces, s0 = (i - b * p.row_pieces) * kPgSlots + lane;
         int32_t *row = p.table + static_cast<size_t>(b) * p.M;
@@ -387,13 +417,13 @@ pages_compact_kernel(const PgParams p) {
 
 static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Workspace: counts of 2 x 256 warps | 4 ints per row | as many ints as the table has
+// Workspace: counts of 2 x 256 warps | 8 ints per row | as many ints as the table has
 // entries (entries, or the list of those that need a page) | 3 lists of pages.
 struct PgWorkspace {
     size_t off_rows, off_entries, off_lists, list, bytes;
     PgWorkspace(int B, int M, int n_pages) {
         off_rows = 2 * kPgWarps * sizeof(int);
-        off_entries = off_rows + align256(4 * static_cast<size_t>(B) * sizeof(int));
+        off_entries = off_rows + align256(8 * static_cast<size_t>(B) * sizeof(int));
         off_lists = off_entries + align256(static_cast<size_t>(B) * M * sizeof(int));
         list = align256(static_cast<size_t>(n_pages) * sizeof(int));
         bytes = off_lists + 3 * list;
