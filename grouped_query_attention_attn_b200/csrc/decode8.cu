@@ -46,7 +46,18 @@
 // A unit that lies in one CTA's run is written by it.  Otherwise its pieces go to
 // the workspace, and the last one to arrive merges them with the log-sum-exp
 // identity.
+//
+// Measured on a B200, 8 K/V heads, d = 128 (share of the 6.47 TB/s copy rate): 64
+// sequences of 1024-8192 keys, groups of 4 or 8: 101 us (95 %); groups of 16: 106 us
+// (90 %); groups of 32: 178 us (54 %, bound by the tensor pipe and two CTAs per SM);
+// a 2048-key window, int8: 50 us (81 %); two sequences of 100000-131072, groups of
+// 8: 79 us (84 %); one sequence of 1024 keys: 7.4 us (bound by latency: three
+// dependent loads, one tile a warp, a merge).  Steps on the way, on the first of
+// these: heads as M rows 176 us; keys as M rows 126; equal runs in place of splits
+// of 1024 keys, seldom-moved reference, loads ahead of the copies 109; no retries at
+// arrival, packed fp32, L2 hint 106; empty places 103; dependent launch 101.
 #include <cmath>
+#include <type_traits>
 
 #include "cache8.cuh"
 
@@ -80,8 +91,8 @@ template <int D, int NT>
 struct D8Layout {
     static constexpr int kTileBytes = kD8Keys * D;          // K or V of one tile
     static constexpr int kStageBytes = 2 * kTileBytes;
-    // TMA ring of one warp: 16 KB for D = 128 and three CTAs per SM, 24 KB for two
-    static constexpr int kStages = (NT == 1 ? 2 : 3) * (128 / D);
+    // TMA ring of one warp: 16 KB with three CTAs per SM, 24 KB with two
+    static constexpr int kStages = (NT <= 2 ? 2 : 3) * (128 / D);
     static constexpr int kRingBytes = kStages * kStageBytes;
     static_assert(kStages <= kD8Epoch, "copies run at most one epoch ahead");
     // the end-of-split merge reuses the rings: per warp 8 NT rows of O, m and l.
@@ -169,8 +180,10 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
+// What shared memory (NT <= 2) and registers (NT = 4) allow.  With 64 sequences of
+// 1024-8192 keys, 8 heads, d = 128 and groups of 16, two CTAs take 113 us and three 106.
 template <int NT>
-constexpr int d8_ctas_per_sm() { return NT == 1 ? 3 : 2; }
+constexpr int d8_ctas_per_sm() { return NT <= 2 ? 3 : 2; }
 
 // NT: tiles of 8 query heads.  kRope: the query is rotated as it is loaded.
 template <int D, int NT, bool kInt8, bool kRope>
@@ -352,22 +365,19 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         load_rows(1, next);
         // Query fragments (column gq of head tile nt).  Contraction step s multiplies
         // elements 4 s .. 4 s + 3 of each thread's quarter of the row (D / 4 elements).
+        // One head tile is kept in registers; of more, each warp prepares one for all.
         constexpr int kQ = D / 4;
-        const __nv_bfloat16 *qg = p.q + grow0 * D + tq * kQ;
-        uint32_t qb[NT][D / 16][2];
-        float2 qs[NT];                                  // score scale of heads 2 tq, 2 tq + 1
+        const int own = NT == 1 ? 0 : warp, own_row = own * 8 + gq;
+        const __nv_bfloat16 *qg = p.q + (grow0 + own_row) * D + tq * kQ;
+        uint32_t qb[D / 16][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + gq;
-#pragma unroll
-            for (int s = 0; s < D / 16; s += 2) {
-                const uint4 w = r < G ? *reinterpret_cast<const uint4 *>(qg + r * D + 4 * s)
-                                      : make_uint4(0u, 0u, 0u, 0u);
-                qb[nt][s][0] = w.x;
-                qb[nt][s][1] = w.y;
-                qb[nt][s + 1][0] = w.z;
-                qb[nt][s + 1][1] = w.w;
-            }
+        for (int s = 0; s < D / 16; s += 2) {
+            const uint4 w = own_row < G ? *reinterpret_cast<const uint4 *>(qg + 4 * s)
+                                        : make_uint4(0u, 0u, 0u, 0u);
+            qb[s][0] = w.x;
+            qb[s][1] = w.y;
+            qb[s + 1][0] = w.z;
+            qb[s + 1][1] = w.w;
         }
         __shared__ float2 rope_cs[kRope ? D / 2 : 1];
         if constexpr (kRope) {
@@ -390,38 +400,47 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int s = 0; s < D / 16; ++s) {
                 const float2 c0 = rope_cs[tq * (kQ / 2) + 2 * s];
                 const float2 c1 = rope_cs[tq * (kQ / 2) + 2 * s + 1];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    qb[nt][s][0] = rope_rotate_pair(qb[nt][s][0], c0.x, c0.y);
-                    qb[nt][s][1] = rope_rotate_pair(qb[nt][s][1], c1.x, c1.y);
-                }
+                qb[s][0] = rope_rotate_pair(qb[s][0], c0.x, c0.y);
+                qb[s][1] = rope_rotate_pair(qb[s][1], c1.x, c1.y);
             }
         }
+        // bring the row's largest value into [1, 2); an infinite or zero row stays as it is
+        float q_max = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // bring the row's largest value into [1, 2); an infinite or zero row stays as it is
-            float mx = 0.0f;
+        for (int s = 0; s < D / 16; ++s) {
+            const float2 a = bf16x2_to_float2(qb[s][0]), c = bf16x2_to_float2(qb[s][1]);
+            q_max = fmaxf(q_max, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(c.x), fabsf(c.y))));
+        }
+        q_max = fmaxf(q_max, __shfl_xor_sync(0xffffffffu, q_max, 1));
+        q_max = fmaxf(q_max, __shfl_xor_sync(0xffffffffu, q_max, 2));
+        const int q_exp = static_cast<int>(__float_as_uint(q_max) >> 23);   // biased exponent
+        const bool fit = q_exp > 0 && q_exp < 255;
+        const uint32_t ex = min(q_exp, 253);            // 2^(ex - 127) and its inverse are normal
+        const float up = fit ? __uint_as_float((254 - ex) << 23) : 1.0f;
+        const float down = (fit ? __uint_as_float(ex << 23) : 1.0f) * p.scale_log2;
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const float2 a = bf16x2_to_float2(qb[nt][s][0]), c = bf16x2_to_float2(qb[nt][s][1]);
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(c.x), fabsf(c.y))));
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 a = bf16x2_to_float2(qb[s][h]);
+                qb[s][h] = pack_f16x2(a.x * up, a.y * up);
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const int e = static_cast<int>(__float_as_uint(mx) >> 23);          // biased exponent
-            const bool fit = e > 0 && e < 255;
-            const uint32_t ex = min(e, 253);            // 2^(ex - 127) and its inverse are normal
-            const float up = fit ? __uint_as_float((254 - ex) << 23) : 1.0f;
-            const float down = (fit ? __uint_as_float(ex << 23) : 1.0f) * p.scale_log2;
-            qs[nt].x = __shfl_sync(0xffffffffu, down, 8 * tq);
-            qs[nt].y = __shfl_sync(0xffffffffu, down, 8 * tq + 4);
+        float2 qs[NT];                                  // score scale of heads 2 tq, 2 tq + 1
+        __shared__ uint4 q_tiles[NT == 1 ? 1 : NT][D / 32][32];      // steps s, s + 1 of a lane
+        __shared__ float2 q_down[NT == 1 ? 1 : NT][4];
+        if constexpr (NT == 1) {
+            qs[0].x = __shfl_sync(0xffffffffu, down, 8 * tq);
+            qs[0].y = __shfl_sync(0xffffffffu, down, 8 * tq + 4);
+        } else {
+            if (own < NT) {                             // (the last piece's tiles have been read)
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
+                for (int s = 0; s < D / 16; s += 2)
+                    q_tiles[own][s / 2][lane] = make_uint4(qb[s][0], qb[s][1], qb[s + 1][0], qb[s + 1][1]);
+                if (tq == 0) reinterpret_cast<float *>(q_down[own])[gq] = down;
+            }
+            __syncthreads();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 a = bf16x2_to_float2(qb[nt][s][h]);
-                    qb[nt][s][h] = pack_f16x2(a.x * up, a.y * up);
-                }
+            for (int nt = 0; nt < NT; ++nt) qs[nt] = q_down[nt][tq];
         }
         // O^T: product j, accumulator e is element (D / 8) gq + 2 j + (e >> 1) of head 2 tq + (e & 1)
         float oacc[NT][D / 16][4];
@@ -472,16 +491,27 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 lds<16 * D>(w[1][0], kt + k_off[0][c]);
                 lds<16 * D>(w[1][1], kt + k_off[1][c]);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int i0 = 0; i0 < 4; i0 += 2) {
+                    uint4 q[NT];                    // steps i0 and i0 + 1
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t a[4];
-                        to_f16x2<kInt8>(w[x][0][i], a[0], a[2]);
-                        to_f16x2<kInt8>(w[x][1][i], a[1], a[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_16816_f16(sacc[nt][x], a, qb[nt][c * 4 + i][0], qb[nt][c * 4 + i][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int s = c * 4 + i0;
+                        q[nt] = NT == 1 ? make_uint4(qb[s][0], qb[s][1], qb[s + 1][0], qb[s + 1][1])
+                                        : q_tiles[nt][s / 2][lane];
                     }
+#pragma unroll
+                    for (int i = i0; i < i0 + 2; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t a[4];
+                            to_f16x2<kInt8>(w[x][0][i], a[0], a[2]);
+                            to_f16x2<kInt8>(w[x][1][i], a[1], a[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16816_f16(sacc[nt][x], a, i == i0 ? q[nt].x : q[nt].z,
+                                              i == i0 ? q[nt].y : q[nt].w);
+                        }
+                }
             }
             // ---- V scales: weight factor of each half, and O's change of units before it;
             //      keys out of sight: a bit of hide_k for half x, key (nb, gq) at 2 x + nb, of
@@ -709,68 +739,90 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
 
         // ---- the last piece of the unit to arrive merges all of them ----
-        __threadfence();                            // my partial rows, device-wide
-        __syncthreads();
+        __syncthreads();                            // the piece's rows are written
         const int pieces = cta1 - cta0 + 1;
         if (threadIdx.x == 0) {
+            __threadfence();                        // ... device-wide
             const bool last = static_cast<int>(atomicAdd(word, 1ull) & 0xFFFFu) + 1 == pieces;
             if (last) *reinterpret_cast<volatile unsigned long long *>(word) = p.call_id << 16;
             merger = last;
+            __threadfence();                        // every piece's rows are visible
         }
         __syncthreads();
         if (!merger) continue;
-        __threadfence();                            // every piece's rows are visible
-        // One warp per head row; D / 4 lanes hold a row's columns, and the other half
-        // of the warp (D = 64) takes every second piece.
+        // Two head rows per warp at a time, D / 4 lanes for a row's columns; the other half
+        // of the warp (D = 64) takes every second piece.  The maximum runs over batches of
+        // pieces, whose lse and rows are loaded together.
         constexpr int kLanes = D / 4, kSub = 32 / kLanes, kBatch = 8;
         const int sub = lane / kLanes, c = lane % kLanes * 4;
         // rows of piece i: slot 1 of the first CTA, slot 0 of the others
-        auto slot = [&](int i) { return (2 * static_cast<size_t>(cta0 + i) + (i == 0)) * G; };
-        for (int r = warp; r < G; r += kD8Warps) {
-            // running maximum over batches, whose lse and rows are loaded together
-            float M = -INFINITY, wsum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto slot = [&](int i) { return (2 * (cta0 + i) + (i == 0)) * G; };
+        auto merge_rows = [&](int r0, auto count) {
+            constexpr int kR = decltype(count)::value;
+            float M[kR], wsum[kR];
+            float4 acc[kR];
+#pragma unroll
+            for (int y = 0; y < kR; ++y) {
+                M[y] = -INFINITY;
+                wsum[y] = 0.0f;
+                acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
             for (int i = 0; i < pieces; i += kSub * kBatch) {
-                float l[kBatch];
-                float4 v[kBatch];
+                float l[kR][kBatch];
+                float4 v[kR][kBatch];
 #pragma unroll
-                for (int x = 0; x < kBatch; ++x) {
-                    const int at = i + x * kSub + sub;
-                    const bool in = at < pieces;
-                    l[x] = in ? __ldcg(p.part_lse + slot(at) + r) : -INFINITY;
-                    v[x] = in ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot(at) + r) * D + c))
-                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
-                float m = M;
+                for (int y = 0; y < kR; ++y)
 #pragma unroll
-                for (int x = 0; x < kBatch; ++x) m = fmaxf(m, l[x]);
-                if constexpr (kSub == 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                if (m == -INFINITY) continue;       // no key in any piece so far
-                const float f = fast_exp2(M - m);
-                M = m;
-                wsum *= f;
-                acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+                    for (int x = 0; x < kBatch; ++x) {
+                        const int at = i + x * kSub + sub;
+                        const bool in = at < pieces;
+                        const size_t row = slot(at) + r0 + y * kD8Warps;
+                        l[y][x] = in ? __ldcg(p.part_lse + row) : -INFINITY;
+                        v[y][x] = in ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + row * D + c))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
 #pragma unroll
-                for (int x = 0; x < kBatch; ++x) {
-                    const float w = fast_exp2(l[x] - M);
-                    wsum += w;
-                    acc.x += w * v[x].x;
-                    acc.y += w * v[x].y;
-                    acc.z += w * v[x].z;
-                    acc.w += w * v[x].w;
+                for (int y = 0; y < kR; ++y) {
+                    float m = M[y];
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) m = fmaxf(m, l[y][x]);
+                    if constexpr (kSub == 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (m == -INFINITY) continue;   // no key in any piece so far
+                    const float f = fast_exp2(M[y] - m);
+                    M[y] = m;
+                    wsum[y] *= f;
+                    float4 a = make_float4(acc[y].x * f, acc[y].y * f, acc[y].z * f, acc[y].w * f);
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) {
+                        const float w = fast_exp2(l[y][x] - m);
+                        wsum[y] += w;
+                        a.x += w * v[y][x].x;
+                        a.y += w * v[y][x].y;
+                        a.z += w * v[y][x].z;
+                        a.w += w * v[y][x].w;
+                    }
+                    acc[y] = a;
                 }
             }
-            if constexpr (kSub == 2) {
-                wsum += __shfl_xor_sync(0xffffffffu, wsum, 16);
-                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-                acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-                acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+#pragma unroll
+            for (int y = 0; y < kR; ++y) {
+                float4 a = acc[y];
+                if constexpr (kSub == 2) {
+                    wsum[y] += __shfl_xor_sync(0xffffffffu, wsum[y], 16);
+                    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+                    a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+                    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+                    a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+                }
+                const float inv = wsum[y] == 0.0f ? 0.0f : 1.0f / wsum[y];
+                if (sub == 0)
+                    *reinterpret_cast<uint2 *>(p.o + (grow0 + r0 + y * kD8Warps) * D + c) = make_uint2(
+                        pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
             }
-            const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
-            if (sub == 0)
-                *reinterpret_cast<uint2 *>(p.o + (grow0 + r) * D + c) = make_uint2(
-                    pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        };
+        for (int r = warp; r < G; r += 2 * kD8Warps) {
+            if (r + kD8Warps < G) merge_rows(r, std::integral_constant<int, 2>{});
+            else merge_rows(r, std::integral_constant<int, 1>{});
         }
         __syncthreads();                            // merger is read
     }
