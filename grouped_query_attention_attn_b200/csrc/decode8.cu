@@ -50,12 +50,12 @@
 // Measured on a B200, 8 K/V heads, d = 128 (share of the 6.47 TB/s copy rate): 64
 // sequences of 1024-8192 keys, groups of 4 or 8: 101 us (95 %); groups of 16: 106 us
 // (90 %); groups of 32: 178 us (54 %, bound by the tensor pipe and two CTAs per SM);
-// a 2048-key window, int8: 50 us (81 %); two sequences of 100000-131072, groups of
-// 8: 79 us (84 %); one sequence of 1024 keys: 7.4 us (bound by latency: three
+// a 2048-key window, int8: 51 us (79 %); two sequences of 100000-131072, groups of
+// 8: 80 us (83 %); one sequence of 1024 keys: 7.4 us (bound by latency: three
 // dependent loads, one tile a warp, a merge).  Steps on the way, on the first of
 // these: heads as M rows 176 us; keys as M rows 126; equal runs in place of splits
 // of 1024 keys, seldom-moved reference, loads ahead of the copies 109; no retries at
-// arrival, packed fp32, L2 hint 106; empty places 103; dependent launch 101.
+// arrival, packed fp32 106; empty places 103; dependent launch 101.
 #include <cmath>
 #include <type_traits>
 
@@ -156,20 +156,15 @@ __device__ __forceinline__ void lds(uint32_t (&r)[2], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]) : "r"(addr), "n"(kOff));
 }
 
-// tma_load_2d of whole 128-byte rows with 32-bit shared-memory addresses.
-// The cache is read once: it should not push the tables, scales and partial results
-// out of L2.
-__device__ __forceinline__ uint64_t evict_first_policy() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ void copy_rows(uint32_t dst, const void *tmap, uint32_t bar, int row,
-                                          uint64_t policy) {
+// 2-D tiled tensor load of whole 128-byte rows into shared memory, completion counted
+// on bar; 32-bit shared-memory addresses.  No L2 hint: marking the stream evict-first
+// saves 1-3 % when no page is shared, and costs 30 % when the sequences share theirs
+// (64 of 8192 keys, four to a prefix: 178 us against 137).
+__device__ __forceinline__ void copy_rows(uint32_t dst, const void *tmap, uint32_t bar, int row) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4}], [%2], %5;"
-        ::"r"(dst), "l"(tmap), "r"(bar), "r"(0), "r"(row), "l"(policy)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(dst), "l"(tmap), "r"(bar), "r"(0), "r"(row)
         : "memory");
 }
 
@@ -246,7 +241,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
             off += __shfl_sync(0xffffffffu, x, 31);
         }
-    const uint64_t policy = evict_first_policy();
     const uint32_t ring_addr = smem_u32(smem + warp * Lay::kRingBytes), bar_addr = smem_u32(full_bar[warp]);
     // where this thread reads a tile: K key d8_key(nb, gq), V key d8_key(k >> 1, 2 tq + (k & 1))
     uint32_t k_off[2][D / 64], v_off[4];
@@ -333,8 +327,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     const bool there = max(row0, row1) >= 0;
                     mbar_expect_tx(&full_bar[warp][sl], there ? Lay::kStageBytes : 0);
                     if (there) {
-                        copy_rows(kt, &tm_k, bar, r / (128 / D), policy);
-                        copy_rows(kt + Lay::kTileBytes, &tm_v, bar, r / (128 / D), policy);
+                        copy_rows(kt, &tm_k, bar, r / (128 / D));
+                        copy_rows(kt + Lay::kTileBytes, &tm_v, bar, r / (128 / D));
                     }
                 } else {
                     mbar_expect_tx(&full_bar[warp][sl],
@@ -344,8 +338,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         const int r = x ? row1 : row0;
                         if (r < 0) continue;
                         const uint32_t dst = kt + x * (Lay::kTileBytes / 2);
-                        copy_rows(dst, &tm_k, bar, r / (128 / D), policy);
-                        copy_rows(dst + Lay::kTileBytes, &tm_v, bar, r / (128 / D), policy);
+                        copy_rows(dst, &tm_k, bar, r / (128 / D));
+                        copy_rows(dst + Lay::kTileBytes, &tm_v, bar, r / (128 / D));
                     }
                 }
             }
@@ -917,6 +911,13 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     if (theta != 0.0f)
         if (int rc = check_theta(theta)) return rc;
     if (B == 0) return GQA_OK;
+    // a windowed sequence reads the tiles of its sinks and of its window
+    long long tiles = d8_tiles(static_cast<long long>(M) * page);
+    if (window > 0 && d8_tiles(window) + 1 + d8_tiles(sinks) < tiles)
+        tiles = d8_tiles(window) + 1 + d8_tiles(sinks);
+    if (static_cast<double>(tiles + kD8Begin) * B * Hkv > 2147483647.0 - kD8MaxCtas)
+        return set_error(GQA_ERR_UNSUPPORTED, "decode8: B=%d x Hkv=%d x M=%d x page=%d rows are too many", B,
+                         Hkv, M, page);
     if (int rc = check_ptr(q, 16, "q")) return rc;
     if (int rc = check_ptr(o, 16, "o")) return rc;
     if (int rc = check_ptr(table, 4, "table")) return rc;
@@ -947,10 +948,6 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     p.block = block;
     p.nblk = page / block;
     p.box = page % kD8Keys == 0 ? kD8Keys : 16;
-    // a windowed sequence reads the tiles of its sinks and of its window
-    long long tiles = d8_tiles(static_cast<long long>(M) * page);
-    if (window > 0 && d8_tiles(window) + 1 + d8_tiles(sinks) < tiles)
-        tiles = d8_tiles(window) + 1 + d8_tiles(sinks);
     p.window = window;
     p.sinks = sinks;
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -960,9 +957,6 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     if (int rc = encode_tmap_rows128(&tk, k_cache, rows, p.box * d / 128)) return rc;
     if (int rc = encode_tmap_rows128(&tv, v_cache, rows, p.box * d / 128)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (static_cast<double>(tiles + kD8Begin) * B * Hkv > 2147483647.0 - kD8MaxCtas)
-        return set_error(GQA_ERR_UNSUPPORTED, "decode8: B=%d x Hkv=%d x M=%d x page=%d rows are too many", B,
-                         Hkv, M, page);
     const bool int8 = kind == GQA_INT8, rope = theta > 0.0f;
     const int G = Hq / Hkv;
     if (d == 128)

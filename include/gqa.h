@@ -350,9 +350,14 @@ int gqa_fold_kv(const void *in, void *out, int B, int T, int H, int g, int d,
  * M * page fit an int (else UNSUPPORTED).  Cache pointers 16-byte, the others
  * 4-byte aligned.  All int32 arrays are DEVICE arrays and are checked by the
  * kernels: a length outside [0, M * page] (clamped) and a table entry outside
- * [0, n_pages) where rows are needed (those rows are left out) are flagged in
- * gqa_device_status as GQA_ERR_INVALID_ARG.  Entries that no row needs are not
- * read as pages.  Scales are finite, 0 or >= 2^-126.
+ * [0, n_pages), or past the M slots, where rows are needed (those rows are left
+ * out) are flagged in gqa_device_status as GQA_ERR_INVALID_ARG.  Entries that no
+ * row needs are not read as pages.  Scales are finite, 0 or >= 2^-126.
+ *
+ * The calls of this cache, gqa_pages_* included, may be captured into CUDA graphs;
+ * make one call of each kind in a CUDA context before the first capture.  Their
+ * kernels are launched as programmatic dependents of the stream's previous kernel
+ * and wait for it to complete before they touch memory.
  */
 
 /*
@@ -370,7 +375,8 @@ int gqa_fold_kv(const void *in, void *out, int B, int T, int H, int g, int d,
  * way from byte * s_old when s > s_old.  +-inf becomes the largest value of its
  * sign; NaN stays NaN in e4m3 and becomes 0 in int8.
  * Needed pages must be in the table and the page that holds row seqlens[b]
- * must belong to one sequence only (gqa_pages_fork sees to that).  k and v
+ * must belong to one sequence only: gqa_pages_fork sees to that, but a sequence
+ * that was cut back into a page it shares must not be appended to.  k and v
  * 16-byte aligned.  T = 0 or B = 0 launches nothing.
  */
 int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
@@ -456,7 +462,7 @@ int gqa_pages_resize(int32_t *table, int32_t *refs, const int32_t *lengths, int 
  * gqa_pages_fork -- row b becomes a copy of the old row parents[b], all rows at
  * once: table, refs and seqlens [B] are rewritten.  parents[b] = b keeps the
  * row, parents[b] < 0 empties it (parents[b] >= B too, flagged INVALID_ARG).
- * Pages full of rows are shared.  The last, partly filled page (and slots past
+ * B <= 49152 (else UNSUPPORTED).  Pages full of rows are shared.  The last, partly filled page (and slots past
  * it) goes to one child: the parent's own row if it stays, else the lowest
  * row; every other child gets a page of its own and a move (src, dst, rows)
  * in moves [1 + B, 3] (written; see gqa_cache8_copy), in row order.

@@ -99,7 +99,7 @@ def test_rows(gqa_lib, call, kw, code):
     (dict(scale=float("nan")), BAD), (dict(theta=-1.0), BAD), (dict(theta=float("inf")), BAD),
     (dict(window=-1), BAD), (dict(sinks=-1), BAD), (dict(q=None), BAD), (dict(o=FAKE + 8), BAD),
     (dict(ws=None), WS), (dict(ws=FAKE + 16), WS), (dict(ws_bytes=64), WS),
-    (dict(B=0, q=None, ws=None), OK)])
+    (dict(B=0, q=None, ws=None), OK), (dict(B=1 << 20, M=1 << 20, ws_bytes=1 << 40), UNS)])
 def test_decode8(gqa_lib, kw, code):
     assert decode8(**kw) == code
 
@@ -118,6 +118,7 @@ def test_pages_pointers(gqa_lib):
     assert resize(B=0, table=None, lens=None) == OK
     assert fork(lens=None) == BAD and fork(parents=FAKE + 1) == BAD and fork(moves=None) == BAD
     assert compact(moves=FAKE + 3) == BAD
+    assert fork(B=49153) == UNS
 
 
 def test_codes_match_the_header():

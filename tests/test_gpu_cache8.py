@@ -613,6 +613,54 @@ def test_a_captured_step(gqa_lib):
     gqa.device_status()
 
 
+def test_a_capture_over_two_streams(gqa_lib):
+    # K / V appended on one stream, the table kept on another, joined before the decode
+    rng = np.random.default_rng(42)
+    p = oc.pool(20, 2, 64, 128, 64, "int8", rng)
+    table, refs, lens = [[-1] * 4 for _ in range(3)], [0] * 20, [64, 100, 30]
+    oc.resize(table, refs, [n + 1 for n in lens], 64)
+    c, t, r, n = to_gpu(p), ints([[-1] * 4 for _ in range(3)]), ints([0] * 20), ints(lens)
+    n1 = n + 1
+    k, v, q = bf16(rng, (3, 1, 2, 128)), bf16(rng, (3, 1, 2, 128)), bf16(rng, (3, 8, 128))
+    oc.append(p, table, lens, [1] * 3, k.double().numpy(), v.double().numpy())
+    want, bound = oc.decode(p, table, [x + 1 for x in lens], q.double().numpy(), 128 ** -0.5)
+    k, v, q = k.cuda(), v.cuda(), q.cuda()
+    o = torch.empty_like(q)
+    other = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        gqa.pages_resize_(t, r, n1, 64)
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            gqa.cache8_append_(c, t, n, k, v)
+        gqa.pages_resize_(t, r, n1, 64)                   # nothing to do
+        here.wait_stream(other)
+        gqa.decode8(q, c, t, n1, out=o)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        o.zero_()
+        g.replay()
+        assert np.all(np.abs(o.double().cpu().numpy() - want) <= bound)
+    assert lists(t) == table and lists(r) == refs
+    same(c, p)
+    gqa.device_status()
+
+
+def test_sequences_that_share_their_pages(gqa_lib):
+    rng, p, table = make(43, "e4m3", 2, 128, 64, 64, [500, 300])
+    t, n = ints([table[0], table[1], table[0], table[0]]), ints([500, 300, 499, 64])
+    q = bf16(rng, (4, 8, 128))
+    o = gqa.decode8(q.cuda(), to_gpu(p), t, n)
+    want, bound = oc.decode(p, lists(t), lists(n), q.double().numpy(), 128 ** -0.5)
+    assert np.all(np.abs(o.double().cpu().numpy() - want) <= bound)
+
+
 def test_large_offsets(gqa_lib):
     # pages past 2^32 bytes of the pool: 36000 pages of 128 KB
     need = 36000 * 8 * 128 * 128 * 2
