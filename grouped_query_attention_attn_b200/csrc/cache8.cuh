@@ -27,14 +27,14 @@ __device__ __forceinline__ void wait_for_stream() {
 }
 
 template <class Kernel, class... Args>
-int launch_dependent(Kernel kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+int launch_dependent(Kernel kern, dim3 grid, dim3 threads, size_t smem, cudaStream_t stream,
                      const char *what, const Args &...args) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = grid;
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
