@@ -69,6 +69,7 @@ constexpr int kD8Threads = kD8Warps * 32;
 constexpr int kD8Begin = 12;                       // what beginning a unit costs, in tiles
 constexpr int kD8Epoch = 16;                       // tiles whose pages a warp's lanes hold
 constexpr int kD8MinTiles = kD8Warps;              // shortest run of a CTA
+constexpr float kD8Merge = 0.25f;                  // merging a piece, in tiles of a run
 constexpr int kD8MaxCtas = 444;                    // 148 SMs x 3 resident CTAs
 constexpr float kD8Least = -3.0e38f;               // reference of a row that has seen no key
 constexpr float kD8Rescale = 8.0f;                 // log2 units: weights stay below 2^8
@@ -205,6 +206,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         tma_prefetch_desc(&tm_v);
     }
     __syncwarp();
+    // RoPE: the turns of each coordinate pair, while the stream's last kernel finishes
+    __shared__ double rope_turn[kRope ? D / 2 : 1];
+    if constexpr (kRope) {
+        for (int i = threadIdx.x; i < D / 2; i += kD8Threads)
+            rope_turn[i] = rope_turns(i, D / 2, p.log_theta);        // read by the same thread
+    }
     dependents_may_launch();
     wait_for_stream();
     // places that each unit of sequence b takes in the line of tiles: kD8Begin empty
@@ -215,10 +222,20 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     };
 
     // ---- this CTA's run of tiles; every warp finds it for itself ----
-    int total = 0;                                  // fits an int (checked on the host)
-    for (int b = lane; b < p.B; b += 32) total += places_of(b);
+    int total = 0, longest = 0;                     // total fits an int (checked on the host)
+    for (int b = lane; b < p.B; b += 32) {
+        const int n = places_of(b);
+        total += n;
+        longest = max(longest, n);
+    }
     total = __reduce_add_sync(0xffffffffu, total) * p.Hkv;
-    const int per = max(kD8MinTiles, (total - 1) / static_cast<int>(gridDim.x) + 1);
+    // A unit of n tiles in runs of r has n / r pieces to merge, one after the other, for
+    // r tiles read side by side by four warps: runs are not shorter than about
+    // sqrt(n kD8Merge), in whole rounds of the warps.  (One unit of 32 heads, d = 64,
+    // 60000 keys: 61 us with runs of 4 tiles at least, 31 so; 1024 keys in 8 units, 7.2.)
+    const int least = static_cast<int>(sqrtf(kD8Merge * __reduce_max_sync(0xffffffffu, longest)));
+    const int per = max((least + kD8Warps) / kD8Warps * kD8Warps,
+                        (total - 1) / static_cast<int>(gridDim.x) + 1);
     int pos = per * blockIdx.x;
     const int end = min(pos + per, total);
     // the sequence it begins in, and that sequence's first tile
@@ -379,7 +396,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int m = max(len - 1, 0);
             for (int i = threadIdx.x; i < D / 2; i += kD8Threads) {
                 float cs, sn;
-                rope_cos_sin(m, rope_turns(i, D / 2, p.log_theta), cs, sn);
+                rope_cos_sin(m, rope_turn[i], cs, sn);
                 rope_cs[i] = make_float2(cs, sn);
             }
         }
@@ -744,7 +761,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         __syncthreads();
         if (!merger) continue;
-        // Two head rows per warp at a time, D / 4 lanes for a row's columns; the other half
+        // Up to four head rows per warp at a time, D / 4 lanes for a row's columns; the other half
         // of the warp (D = 64) takes every second piece.  The maximum runs over batches of
         // pieces, whose lse and rows are loaded together.
         constexpr int kLanes = D / 4, kSub = 32 / kLanes, kBatch = 8;
@@ -814,9 +831,18 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
             }
         };
-        for (int r = warp; r < G; r += 2 * kD8Warps) {
-            if (r + kD8Warps < G) merge_rows(r, std::integral_constant<int, 2>{});
-            else merge_rows(r, std::integral_constant<int, 1>{});
+        constexpr int kMost = NT == 4 ? 4 : 2;      // four rows spill with 168 registers
+        for (int r = warp; r < G;) {
+            if (kMost == 4 && r + 3 * kD8Warps < G) {
+                merge_rows(r, std::integral_constant<int, kMost>{});
+                r += 4 * kD8Warps;
+            } else if (r + kD8Warps < G) {
+                merge_rows(r, std::integral_constant<int, 2>{});
+                r += 2 * kD8Warps;
+            } else {
+                merge_rows(r, std::integral_constant<int, 1>{});
+                r += kD8Warps;
+            }
         }
         __syncthreads();                            // merger is read
     }

@@ -149,7 +149,8 @@ def test_workspace_covers_every_cut(gqa_lib, B, Hkv, G, tiles):
     for _ in range(20):
         n = [rng.choice([0, 1, tiles, rng.randint(0, tiles)]) for _ in range(min(B, 40)) for _ in range(Hkv)]
         total = sum(x + 12 for x in n if x)
-        per = max(4, -(-total // ctas))
+        least = int((0.25 * max(x + 12 if x else 0 for x in n)) ** 0.5)
+        per = max((least + 4) // 4 * 4, -(-total // ctas))
         assert -(-total // per) <= ctas
         at = 0
         begun, carried = [0] * ctas, [0] * ctas
