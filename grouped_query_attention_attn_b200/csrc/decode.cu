@@ -464,7 +464,7 @@ size_t decode_workspace_bytes(int B, int Hq, int Hkv, int d, int Lmax) {
 // Per-call ids for the arrival words: 48 bits, never 0, different for every
 // launch of the process (the start is drawn from the clock, so a workspace
 // reused by another process is unlikely to hold a matching word either).
-unsigned long long next_call_id() {
+static unsigned long long next_call_id() {
     static std::atomic<unsigned long long> counter{
         static_cast<unsigned long long>(
             std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull};

@@ -56,6 +56,8 @@
 // these: heads as M rows 176 us; keys as M rows 126; equal runs in place of splits
 // of 1024 keys, seldom-moved reference, loads ahead of the copies 109; no retries at
 // arrival, packed fp32 106; empty places 103; dependent launch 101.
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <type_traits>
 
@@ -138,6 +140,16 @@ __device__ __forceinline__ uint32_t d8_off(int key, int c) {
 template <int D>
 __device__ __forceinline__ int d8_key(int nb, int n) {
     return D == 128 ? nb * 8 + n : 4 * (n >> 1) + 2 * nb + (n & 1);
+}
+
+// D (16x8, fp32) += A (16x16) B (16x8), f16 operands.
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -854,6 +866,19 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int i = threadIdx.x; i < p.Hq * D / 8; i += kD8Threads)
                 reinterpret_cast<uint4 *>(p.o + static_cast<size_t>(z) * p.Hq * D)[i] =
                     make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// Per-call ids for the arrival words: 48 bits, never 0, different for every launch of the
+// process; the start is drawn from the clock, so that what another process or the
+// other decode left in a workspace is unlikely to match.
+static unsigned long long next_call_id() {
+    static std::atomic<unsigned long long> counter{
+        static_cast<unsigned long long>(
+            std::chrono::steady_clock::now().time_since_epoch().count()) * 0xD6E8FEB86659FD93ull};
+    for (;;) {
+        const unsigned long long id = counter.fetch_add(1) & 0xFFFFFFFFFFFFull;
+        if (id != 0) return id;
     }
 }
 

@@ -94,10 +94,6 @@ int check_scale(float scale);
 int check_theta(float theta);
 int check_workspace(const void *workspace, size_t bytes, size_t need);
 
-// Per-call ids for arrival words in a decode workspace: 48 bits, never 0,
-// different for every launch of the process.
-unsigned long long next_call_id();
-
 // ---- launchers (arguments already validated by the C-ABI layer) ----------
 int launch_fwd_f32(const float *q, const float *k, const float *v, float *o, float *lse,
                    int B, int Tq, int Tkv, int Hq, int Hkv, int d, int causal, float scale,
