@@ -101,7 +101,7 @@ cache8_append_kernel(const ApParams p) {
     const bool bad = start < 0 || start > p.M * p.c.page || count < 0 || count > p.T;
     const int skip = start % block;                 // older rows of the first block
     const int t0 = static_cast<int>(blockIdx.y) * block - skip;  // new row of the block's first row
-    if (!bad && t0 >= count) return;
+    if (!bad && (t0 >= count || count == 0)) return;             // no new row (count 0 in mid-block)
     if (bad) count = t0;                            // no rows
     const int r0 = max(0, -t0), r1 = min(block, count - t0);
 

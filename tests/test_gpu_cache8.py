@@ -356,6 +356,18 @@ def test_append_leaves_other_rows_and_flags_bad_ones(gqa_lib):
 
 # -------------------------------------------------------------- read, copy --
 
+def test_append_of_no_rows_needs_no_page(gqa_lib):
+    # rows that add nothing, ending inside a block: their pages may be gone or be shared
+    rng, p, table = make(16, "e4m3", 2, 128, 64, 16, [5, 70, 23], extra=20)
+    c, lens, counts = to_gpu(p), [5, 70, 23], [0, 0, 9]
+    k, v = bf16(rng, (3, 9, 2, 128)), bf16(rng, (3, 9, 2, 128))
+    gone = [[-1] * len(table[0]), [table[1][0], table[2][0]] + [-1] * (len(table[1]) - 2), table[2]]
+    gqa.cache8_append_(c, ints(gone), ints(lens), k.cuda(), v.cuda(), ints(counts))
+    gqa.device_status()
+    oc.append(p, [table[2]], [23], [9], k[2:].double().numpy(), v[2:].double().numpy())
+    same(c, p)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("page,block,T", [(16, 16, 1), (48, 16, 100), (64, 32, 333), (128, 128, 17), (1024, 256, 40)])
