@@ -253,7 +253,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // the sequence it begins in, and that sequence's first tile
     int b = 0, off = 0;
     if (pos < end)
-        for (int b0 = 0;; b0 += 32) {               // ends: pos < total
+        for (int b0 = 0; b0 < p.B; b0 += 32) {      // one is found: pos < total
             const int n = b0 + lane < p.B ? places_of(b0 + lane) * p.Hkv : 0;
             int x = n;                              // inclusive prefix sum
 #pragma unroll
@@ -285,7 +285,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
     int st = 0;                                     // the warp's place in its ring, and its phase
     uint32_t ph = 0;
-    while (pos < end) {
+    // (b < B and kvh < Hkv hold by the sums above; they are checked so that lengths which
+    // change under the kernel can end it early, but not lead it astray)
+    while (pos < end && b < p.B) {
         const int len = p.seqlens[b], L = min(max(len, 0), Lmax);
         const D8Tiles seq(L, p.window, p.sinks);
         if (seq.n == 0) {
@@ -294,11 +296,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         // ---- the piece: tiles first .. first + count - 1 of unit (b, kvh) ----
         const int places = seq.n + kD8Begin, kvh = (pos - off) / places;
+        if (static_cast<unsigned>(kvh) >= static_cast<unsigned>(p.Hkv)) break;
         const int tile0 = off + kvh * places + kD8Begin;         // place of the unit's first tile
         const int stop = min(tile0 + seq.n, end), first = max(pos - tile0, 0);
         const int count = stop - (tile0 + first);
         // CTAs whose runs hold the unit's first and last tile
-        const int cta0 = tile0 / per, cta1 = (tile0 + seq.n - 1) / per;
+        const int cta0 = tile0 / per, cta1 = min((tile0 + seq.n - 1) / per, static_cast<int>(gridDim.x) - 1);
         const size_t grow0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(kvh) * G;
         const size_t unit = static_cast<size_t>(b) * p.Hkv + kvh;
         const int32_t *row = p.table + static_cast<size_t>(b) * p.M;

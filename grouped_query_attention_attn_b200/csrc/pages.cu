@@ -34,6 +34,7 @@ constexpr int kPgWarps = kPgCtas * kPgThreads / 32;
 // Everything the cluster's threads wrote before is visible to its threads after
 // (release and acquire at cluster scope, global memory included).
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();                             // the aligned form wants whole warps
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -352,7 +352,8 @@ int gqa_fold_kv(const void *in, void *out, int B, int T, int H, int g, int d,
  * kernels: a length outside [0, M * page] (clamped) and a table entry outside
  * [0, n_pages), or past the M slots, where rows are needed (those rows are left
  * out) are flagged in gqa_device_status as GQA_ERR_INVALID_ARG.  Entries that no
- * row needs are not read as pages.  Scales are finite, 0 or >= 2^-126.
+ * row needs are not read as pages.  Scales are finite, 0 or >= 2^-126.  Nothing
+ * else may write them, or the rows that are read, while a call runs.
  *
  * The calls of this cache, gqa_pages_* included, may be captured into CUDA graphs;
  * make one call of each kind in a CUDA context before the first capture.  Their
@@ -377,7 +378,9 @@ int gqa_fold_kv(const void *in, void *out, int B, int T, int H, int g, int d,
  * Needed pages must be in the table and the page that holds row seqlens[b]
  * must belong to one sequence only: gqa_pages_fork sees to that, but a sequence
  * that was cut back into a page it shares must not be appended to.  k and v
- * 16-byte aligned.  T = 0 or B = 0 launches nothing.
+ * 16-byte aligned.  A sequence with counts[b] = 0 needs no page.  B and the number
+ * of blocks that T rows can touch are at most 65535 (else UNSUPPORTED).  T = 0 or
+ * B = 0 launches nothing.
  */
 int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
                       const int32_t *table, const int32_t *seqlens, const int32_t *counts,
@@ -441,8 +444,8 @@ int gqa_decode8(const void *q, const void *k_cache, const void *v_cache, const f
  * the device; pages are taken lowest first, for the entries that need one in
  * (row, slot) order.  A pool with too few free pages leaves the last entries at
  * -1 and flags GQA_ERR_PAGES in gqa_device_status; table entries >= n_pages,
- * lengths outside [0, M * page] (clamped) and counts that would fall below 0
- * flag GQA_ERR_INVALID_ARG.  One cache per layer can share a table: the calls
+ * lengths outside [0, M * page] (clamped) and, in gqa_pages_resize, counts that
+ * would fall below 0 flag GQA_ERR_INVALID_ARG.  One cache per layer can share a table: the calls
  * return the page moves to apply to each with gqa_cache8_copy.  workspace:
  * >= gqa_pages_workspace_size(B, M, n_pages) bytes, 256-byte aligned, contents on
  * entry irrelevant, one for each call in flight.
