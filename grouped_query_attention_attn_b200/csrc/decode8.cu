@@ -58,6 +58,7 @@
 // arrival, packed fp32 106; empty places 103; dependent launch 101.
 #include <atomic>
 #include <chrono>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -83,7 +84,9 @@ struct D8Params {
     __nv_bfloat16 *o;
     float *part_o, *part_lse;                      // two pieces of G rows per CTA
     unsigned long long *arrivals, call_id;
-    int B, Hq, Hkv, M, n_pages, page, nblk, block, box;   // box: keys per TMA box
+    int B, Hq, Hkv, M, n_pages, page, nblk, box;          // box: keys per TMA box
+    unsigned long long page_inv;                   // ceil(2^35 / (page / 16))
+    uint32_t block_inv;                            // ceil(2^16 / (block / 16))
     int window, sinks;
     float scale_log2;
     double log_theta;
@@ -250,11 +253,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         (total - 1) / static_cast<int>(gridDim.x) + 1);
     int pos = per * blockIdx.x;
     const int end = min(pos + per, total);
-    // the sequence it begins in, and that sequence's first tile
-    int b = 0, off = 0;
+    // the unit it begins in: sequence b, K/V head kvh, place of its first tile
+    int b = 0, kvh = 0, tile0 = 0;
     if (pos < end)
-        for (int b0 = 0; b0 < p.B; b0 += 32) {      // one is found: pos < total
-            const int n = b0 + lane < p.B ? places_of(b0 + lane) * p.Hkv : 0;
+        for (int b0 = 0, off = 0; b0 < p.B; b0 += 32) {          // one is found: pos < total
+            const int places = b0 + lane < p.B ? places_of(b0 + lane) : 0, n = places * p.Hkv;
             int x = n;                              // inclusive prefix sum
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -264,8 +267,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const uint32_t past = __ballot_sync(0xffffffffu, pos < off + x);
             if (past) {
                 const int l = __ffs(past) - 1;      // first sequence that ends past pos
+                const int each = __shfl_sync(0xffffffffu, places, l);
                 b = b0 + l;
                 off += __shfl_sync(0xffffffffu, x - n, l);
+                kvh = (pos - off) / each;
+                tile0 = off + kvh * each + kD8Begin;
                 break;
             }
             off += __shfl_sync(0xffffffffu, x, 31);
@@ -283,10 +289,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         v_off[k] = d8_off<D>(d8_key<D>(k >> 1, 2 * tq + (k & 1)), D == 128 ? gq : gq >> 1) +
                    (D == 128 ? 0 : (gq & 1) * 8);
 
+    __shared__ float2 rope_cs[kRope ? D / 2 : 1];
+    int rope_len = INT_MIN;                         // the length whose turns it holds
     int st = 0;                                     // the warp's place in its ring, and its phase
     uint32_t ph = 0;
-    // (b < B and kvh < Hkv hold by the sums above; they are checked so that lengths which
-    // change under the kernel can end it early, but not lead it astray)
+    // (b < B holds by the sums above; it is checked so that lengths which change under
+    // the kernel can end the run early, but not lead it astray)
     while (pos < end && b < p.B) {
         const int len = p.seqlens[b], L = min(max(len, 0), Lmax);
         const D8Tiles seq(L, p.window, p.sinks);
@@ -295,20 +303,22 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             continue;
         }
         // ---- the piece: tiles first .. first + count - 1 of unit (b, kvh) ----
-        const int places = seq.n + kD8Begin, kvh = (pos - off) / places;
-        if (static_cast<unsigned>(kvh) >= static_cast<unsigned>(p.Hkv)) break;
-        const int tile0 = off + kvh * places + kD8Begin;         // place of the unit's first tile
-        const int stop = min(tile0 + seq.n, end), first = max(pos - tile0, 0);
-        const int count = stop - (tile0 + first);
+        const int head = kvh, unit_end = tile0 + seq.n, stop = min(unit_end, end);
+        const int first = max(pos - tile0, 0), count = stop - (tile0 + first);
         // CTAs whose runs hold the unit's first and last tile
-        const int cta0 = tile0 / per, cta1 = min((tile0 + seq.n - 1) / per, static_cast<int>(gridDim.x) - 1);
-        const size_t grow0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(kvh) * G;
-        const size_t unit = static_cast<size_t>(b) * p.Hkv + kvh;
+        int cta0 = blockIdx.x, cta1 = blockIdx.x;
+        if (first > 0) cta0 = tile0 / per;
+        if (unit_end > end) cta1 = min((unit_end - 1) / per, static_cast<int>(gridDim.x) - 1);
+        const size_t grow0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(head) * G;
+        const size_t unit = static_cast<size_t>(b) * p.Hkv + head;
         const int32_t *row = p.table + static_cast<size_t>(b) * p.M;
         pos = stop;                                 // (a run may end in the empty places)
-        if (kvh == p.Hkv - 1 && pos == tile0 + seq.n) {          // on to the next sequence
-            off += p.Hkv * places;
-            ++b;
+        if (pos == unit_end) {                      // on to the next unit
+            tile0 = unit_end + kD8Begin;
+            if (++kvh == p.Hkv) {
+                kvh = 0;
+                ++b;
+            }
         }
         if (count <= 0) continue;
         const int n_iter = (count - warp + kD8Warps - 1) / kD8Warps;      // tiles of this warp
@@ -318,10 +328,10 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         };
         // Lane i holds what is known of the 16 keys that are half i & 1 of tile i >> 1 of
         // an epoch: their first row in the cache (-1: not there; fits an int, checked on
-        // the host), its place in the page, and the scales.  The V scale is negated where
+        // the host), the place of their scales, and these.  The V scale is negated where
         // some of the keys are out of sight, and -inf where none is there.
         struct Group {
-            int row, off;
+            int row, at;
             float ks, vs;
         };
         auto load_rows = [&](int epoch, Group &g) {
@@ -329,22 +339,25 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int key = key_of(t) + (lane & 1) * 16;
             g.row = -1;
             if (t < n_iter && seen(key, 16)) {      // key < L: the slot exists
-                const int page = row[key / p.page];
-                g.off = key % p.page;
-                if (page >= 0 && page < p.n_pages)
-                    g.row = (page * p.Hkv + kvh) * p.page + g.off;
-                else
+                // key / 16 < 2^27 and page / 16 <= 64: the product is exact enough
+                const int slot = static_cast<int>((static_cast<uint32_t>(key) >> 4) * p.page_inv >> 35);
+                const int page = row[slot], off = key - slot * p.page;
+                if (page >= 0 && page < p.n_pages) {
+                    const int ph = page * p.Hkv + head;
+                    g.row = ph * p.page + off;
+                    g.at = ph * p.nblk + static_cast<int>((static_cast<uint32_t>(off) >> 4) * p.block_inv >> 16);
+                } else {
                     record_status(p.status, GQA_ERR_INVALID_ARG);
+                }
             }
         };
         auto load_scales = [&](int epoch, Group &g) {
             g.ks = 0.0f;
             g.vs = -INFINITY;
             if (g.row >= 0) {
-                const size_t at = static_cast<size_t>((g.row - g.off) / p.page) * p.nblk + g.off / p.block;
                 const int key = key_of(epoch * kD8Epoch + (lane >> 1)) + (lane & 1) * 16;
-                g.ks = p.k_scale[at];
-                g.vs = p.v_scale[at];
+                g.ks = p.k_scale[g.at];
+                g.vs = p.v_scale[g.at];
                 if (!(key + 16 <= L && (key >= seq.lo || key + 16 <= seq.sinks))) g.vs = -g.vs;
             }
         };
@@ -405,9 +418,10 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             qb[s + 1][0] = w.z;
             qb[s + 1][1] = w.w;
         }
-        __shared__ float2 rope_cs[kRope ? D / 2 : 1];
-        if constexpr (kRope) {
-            __syncthreads();                        // the last piece's table is read
+        const bool turn = kRope && rope_len != len; // else they are the last piece's
+        if (turn) {
+            __syncthreads();                        // the last piece's turns are read
+            rope_len = len;
             const int m = max(len - 1, 0);
             for (int i = threadIdx.x; i < D / 2; i += kD8Threads) {
                 float cs, sn;
@@ -421,7 +435,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (threadIdx.x == 0 && cta0 != cta1 && (left >> 16) != p.call_id)
             atomicCAS(word, left, p.call_id << 16);
         if constexpr (kRope) {
-            __syncthreads();
+            if (turn) __syncthreads();
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
                 const float2 c0 = rope_cs[tq * (kQ / 2) + 2 * s];
@@ -999,7 +1013,8 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     p.M = M;
     p.n_pages = n_pages;
     p.page = page;
-    p.block = block;
+    p.page_inv = ((1ull << 35) + page / 16 - 1) / (page / 16);
+    p.block_inv = ((1u << 16) + block / 16 - 1) / (block / 16);
     p.nblk = page / block;
     p.box = page % kD8Keys == 0 ? kD8Keys : 16;
     p.window = window;
