@@ -43,13 +43,19 @@
 // rescaled, as for a new maximum.  vref never falls by more than 2^64 at once,
 // which keeps O finite; weights of a smaller block are below 2^-64 vref.
 //
+// Groups of 17-32 heads are shared by two CTAs (blockIdx.y), which read the same run at
+// the same time, once from HBM and once from L2.  With all 32 heads in one CTA the
+// accumulators allow two CTAs per SM, a tile takes a warp twice as long and the merge has
+// twice the rows: four sequences of 8192 keys, one K/V head, 24.2 us against 19.6; one of
+// 1000, 13.7 against 10.1; 64 of 4608, eight K/V heads, 177 against 184.
+//
 // A unit that lies in one CTA's run is written by it.  Otherwise its pieces go to
 // the workspace, and the last one to arrive merges them with the log-sum-exp
 // identity.
 //
 // Measured on a B200, 8 K/V heads, d = 128 (share of the 6.47 TB/s copy rate): 64
 // sequences of 1024-8192 keys, groups of 4 or 8: 101 us (95 %); groups of 16: 106 us
-// (90 %); groups of 32: 178 us (54 %, bound by the tensor pipe and two CTAs per SM);
+// (90 %); groups of 32: 184 us (51 %, bound by the products: two CTAs convert each tile);
 // a 2048-key window, int8: 51 us (79 %); two sequences of 100000-131072, groups of
 // 8: 80 us (83 %); one sequence of 1024 keys: 7.4 us (bound by latency: three
 // dependent loads, one tile a warp, a merge).  Steps on the way, on the first of
@@ -73,7 +79,9 @@ constexpr int kD8Begin = 12;                       // what beginning a unit cost
 constexpr int kD8Epoch = 16;                       // tiles whose pages a warp's lanes hold
 constexpr int kD8MinTiles = kD8Warps;              // shortest run of a CTA
 constexpr float kD8Merge = 0.25f;                  // merging a piece, in tiles of a run
-constexpr int kD8MaxCtas = 444;                    // 148 SMs x 3 resident CTAs
+constexpr int kD8CtasPerSm = 3;                    // what shared memory and registers allow
+constexpr int kD8MaxCtas = 148 * kD8CtasPerSm;     // all resident
+constexpr int kD8Heads = 16;                       // query heads of a CTA at most
 constexpr float kD8Least = -3.0e38f;               // reference of a row that has seen no key
 constexpr float kD8Rescale = 8.0f;                 // log2 units: weights stay below 2^8
 
@@ -82,9 +90,10 @@ struct D8Params {
     const float *k_scale, *v_scale;
     const int32_t *table, *seqlens;
     __nv_bfloat16 *o;
-    float *part_o, *part_lse;                      // two pieces of G rows per CTA
+    float *part_o, *part_lse;                      // two pieces of `share` rows per CTA
     unsigned long long *arrivals, call_id;
     int B, Hq, Hkv, M, n_pages, page, nblk, box;          // box: keys per TMA box
+    int share;                                     // heads of a group per CTA (blockIdx.y)
     unsigned long long page_inv;                   // ceil(2^35 / (page / 16))
     uint32_t block_inv;                            // ceil(2^16 / (block / 16))
     int window, sinks;
@@ -97,8 +106,8 @@ template <int D, int NT>
 struct D8Layout {
     static constexpr int kTileBytes = kD8Keys * D;          // K or V of one tile
     static constexpr int kStageBytes = 2 * kTileBytes;
-    // TMA ring of one warp: 16 KB with three CTAs per SM, 24 KB with two
-    static constexpr int kStages = (NT <= 2 ? 2 : 3) * (128 / D);
+    // TMA ring of one warp: 16 KB, with three CTAs per SM
+    static constexpr int kStages = 2 * (128 / D);
     static constexpr int kRingBytes = kStages * kStageBytes;
     static_assert(kStages <= kD8Epoch, "copies run at most one epoch ahead");
     // the end-of-split merge reuses the rings: per warp 8 NT rows of O, m and l.
@@ -191,14 +200,9 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
-// What shared memory (NT <= 2) and registers (NT = 4) allow.  With 64 sequences of
-// 1024-8192 keys, 8 heads, d = 128 and groups of 16, two CTAs take 113 us and three 106.
-template <int NT>
-constexpr int d8_ctas_per_sm() { return NT <= 2 ? 3 : 2; }
-
 // NT: tiles of 8 query heads.  kRope: the query is rotated as it is loaded.
 template <int D, int NT, bool kInt8, bool kRope>
-__global__ void __launch_bounds__(kD8Threads, d8_ctas_per_sm<NT>())
+__global__ void __launch_bounds__(kD8Threads, kD8CtasPerSm)
 decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const D8Params p) {
     using Lay = D8Layout<D, NT>;
@@ -211,7 +215,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;        // quad, lane in quad
-    const int G = p.Hq / p.Hkv;
+    const int G = min(p.share, p.Hq / p.Hkv - static_cast<int>(blockIdx.y) * p.share);   // heads here
+    const int cta = blockIdx.y * gridDim.x + blockIdx.x;
     const int Lmax = p.M * p.page;
     if (lane == 0) {
         abort_flag[warp] = 0;
@@ -309,8 +314,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         int cta0 = blockIdx.x, cta1 = blockIdx.x;
         if (first > 0) cta0 = tile0 / per;
         if (unit_end > end) cta1 = min((unit_end - 1) / per, static_cast<int>(gridDim.x) - 1);
-        const size_t grow0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(head) * G;
         const size_t unit = static_cast<size_t>(b) * p.Hkv + head;
+        const size_t grow0 = unit * (p.Hq / p.Hkv) + blockIdx.y * p.share;
         const int32_t *row = p.table + static_cast<size_t>(b) * p.M;
         pos = stop;                                 // (a run may end in the empty places)
         if (pos == unit_end) {                      // on to the next unit
@@ -395,7 +400,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // (whatever another call, or uninitialised memory, left there; if the exchange
         // fails, another piece has claimed it), so that an arrival is one addition.  The
         // last one leaves (call id, 0) for a replay of the same launch.
-        unsigned long long *word = p.arrivals + unit, left = 0;
+        unsigned long long *word = p.arrivals + unit * gridDim.y + blockIdx.y, left = 0;
         if (threadIdx.x == 0 && cta0 != cta1) left = *reinterpret_cast<volatile unsigned long long *>(word);
         // Loads that nothing waits for yet come first: once the copies of all CTAs are
         // under way, a load takes several microseconds.
@@ -766,7 +771,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
             } else {
                 // slot 0 of the CTA: a unit that an earlier run began; slot 1: begun here
-                const size_t at = (2 * static_cast<size_t>(blockIdx.x) + (first == 0)) * G + r;
+                const size_t at = (2 * static_cast<size_t>(cta) + (first == 0)) * p.share + r;
                 *reinterpret_cast<float4 *>(p.part_o + at * D + c) = acc;
                 if (c == 0) p.part_lse[at] = wsum == 0.0f ? -INFINITY : M + __log2f(wsum);
             }
@@ -790,13 +795,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         __syncthreads();
         if (!merger) continue;
-        // Up to four head rows per warp at a time, D / 4 lanes for a row's columns; the other half
+        // One or two head rows per warp at a time, D / 4 lanes for a row's columns; the other half
         // of the warp (D = 64) takes every second piece.  The maximum runs over batches of
         // pieces, whose lse and rows are loaded together.
         constexpr int kLanes = D / 4, kSub = 32 / kLanes, kBatch = 8;
         const int sub = lane / kLanes, c = lane % kLanes * 4;
         // rows of piece i: slot 1 of the first CTA, slot 0 of the others
-        auto slot = [&](int i) { return (2 * (cta0 + i) + (i == 0)) * G; };
+        const int slot0 = blockIdx.y * gridDim.x + cta0;
+        auto slot = [&](int i) { return (2 * (slot0 + i) + (i == 0)) * p.share; };
         auto merge_rows = [&](int r0, auto count) {
             constexpr int kR = decltype(count)::value;
             float M[kR], wsum[kR];
@@ -860,12 +866,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
             }
         };
-        constexpr int kMost = NT == 4 ? 4 : 2;      // four rows spill with 168 registers
-        for (int r = warp; r < G;) {
-            if (kMost == 4 && r + 3 * kD8Warps < G) {
-                merge_rows(r, std::integral_constant<int, kMost>{});
-                r += 4 * kD8Warps;
-            } else if (r + kD8Warps < G) {
+        for (int r = warp; r < G;) {                // (four rows would spill)
+            if (r + kD8Warps < G) {
                 merge_rows(r, std::integral_constant<int, 2>{});
                 r += 2 * kD8Warps;
             } else {
@@ -876,7 +878,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         __syncthreads();                            // merger is read
     }
     // sequences without a visible key: zeros; lengths outside the table: flagged
-    for (int z = blockIdx.x; z < p.B; z += gridDim.x) {
+    for (int z = cta; z < p.B; z += gridDim.x * gridDim.y) {
         if (threadIdx.x == 0 && (p.seqlens[z] < 0 || p.seqlens[z] > Lmax))
             record_status(p.status, GQA_ERR_INVALID_ARG);
         if (places_of(z) == 0)
@@ -909,15 +911,21 @@ static int d8_grid(int B, int Hkv, long long tiles, int most) {
 
 static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Workspace: partial O [CTAs, 2, G, d] fp32 | partial lse [CTAs, 2, G] fp32 (log2
-// units) | arrival words [B, Hkv] u64.
+// CTAs that split the heads of a group, and the heads that each takes.
+static int d8_groups(int G) { return (G + kD8Heads - 1) / kD8Heads; }
+static int d8_share(int G) { return (G - 1) / d8_groups(G) + 1; }
+
+// Workspace: partial O [CTAs, 2, heads per CTA, d] fp32 | partial lse [CTAs, 2, heads per
+// CTA] fp32 (log2 units) | arrival words [B, Hkv, CTAs of a group] u64.
 struct D8Workspace {
     size_t off_lse, off_arrivals, bytes;
     D8Workspace(int B, int Hq, int Hkv, int d, long long Lmax) {
-        const size_t ctas = d8_grid(B, Hkv, d8_tiles(Lmax), kD8MaxCtas), rows = ctas * 2 * (Hq / Hkv);
+        const int G = Hq / Hkv, groups = d8_groups(G);
+        const size_t ctas = static_cast<size_t>(d8_grid(B, Hkv, d8_tiles(Lmax), kD8MaxCtas / groups)) * groups;
+        const size_t rows = ctas * 2 * d8_share(G);
         off_lse = align256(rows * d * sizeof(float));
         off_arrivals = off_lse + align256(rows * sizeof(float));
-        bytes = off_arrivals + align256(static_cast<size_t>(B) * Hkv * 8);
+        bytes = off_arrivals + align256(static_cast<size_t>(B) * Hkv * groups * 8);
     }
 };
 
@@ -934,8 +942,9 @@ static int launch_decode8_kernel(const CUtensorMap &tk, const CUtensorMap &tv, c
         return rc;
     int n_sm = 0;
     if (int rc = sm_count(&n_sm)) return rc;
-    const int most = min(kD8MaxCtas, n_sm * d8_ctas_per_sm<NT>());     // all resident at once
-    return launch_dependent(kern, d8_grid(p.B, p.Hkv, tiles, most), kD8Threads, smem, stream,
+    const int groups = d8_groups(p.Hq / p.Hkv);
+    const int most = min(kD8MaxCtas, n_sm * kD8CtasPerSm) / groups;    // all resident at once
+    return launch_dependent(kern, dim3(d8_grid(p.B, p.Hkv, tiles, most), groups), kD8Threads, smem, stream,
                             "decode8_kernel launch", tk, tv, p);
 }
 
@@ -1007,6 +1016,7 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     p.part_lse = reinterpret_cast<float *>(base + ws.off_lse);
     p.arrivals = reinterpret_cast<unsigned long long *>(base + ws.off_arrivals);
     p.call_id = next_call_id();
+    p.share = d8_share(Hq / Hkv);
     p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;
@@ -1027,12 +1037,9 @@ extern "C" int gqa_decode8(const void *q, const void *k_cache, const void *v_cac
     if (int rc = encode_tmap_rows128(&tv, v_cache, rows, p.box * d / 128)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool int8 = kind == GQA_INT8, rope = theta > 0.0f;
-    const int G = Hq / Hkv;
     if (d == 128)
-        return G <= 8    ? launch_decode8_kind<128, 1>(int8, rope, tk, tv, p, tiles, s)
-               : G <= 16 ? launch_decode8_kind<128, 2>(int8, rope, tk, tv, p, tiles, s)
-                         : launch_decode8_kind<128, 4>(int8, rope, tk, tv, p, tiles, s);
-    return G <= 8    ? launch_decode8_kind<64, 1>(int8, rope, tk, tv, p, tiles, s)
-           : G <= 16 ? launch_decode8_kind<64, 2>(int8, rope, tk, tv, p, tiles, s)
-                     : launch_decode8_kind<64, 4>(int8, rope, tk, tv, p, tiles, s);
+        return p.share <= 8 ? launch_decode8_kind<128, 1>(int8, rope, tk, tv, p, tiles, s)
+                            : launch_decode8_kind<128, 2>(int8, rope, tk, tv, p, tiles, s);
+    return p.share <= 8 ? launch_decode8_kind<64, 1>(int8, rope, tk, tv, p, tiles, s)
+                        : launch_decode8_kind<64, 2>(int8, rope, tk, tv, p, tiles, s);
 }
