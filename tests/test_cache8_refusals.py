@@ -137,14 +137,16 @@ def test_workspace_sizes(gqa_lib):
     assert b.gqa_pages_workspace_size(4, 4, 16) % 256 == 0 and b.gqa_pages_workspace_size(4, 0, 16) == 0
 
 
-@pytest.mark.parametrize("B,Hkv,G", [(1, 1, 1), (1, 8, 4), (3, 5, 7), (64, 8, 4), (1000, 8, 32)])
+@pytest.mark.parametrize("B,Hkv,G", [(1, 1, 1), (1, 8, 4), (3, 5, 7), (64, 8, 4), (2, 3, 17), (1000, 8, 32)])
 @pytest.mark.parametrize("tiles", [1, 4, 5, 33, 1000, 16384])
 def test_workspace_covers_every_cut(gqa_lib, B, Hkv, G, tiles):
     # the units (sequence, head), 12 empty places and their tiles each, in equal runs of
-    # at least 4 places, at most 444: each CTA writes at most two pieces of G rows
+    # at least 4 places: each CTA writes at most two pieces of its rows.  At most 444 CTAs,
+    # 16 heads in each, so that those of a larger group share a run
     got = b.gqa_decode8_workspace_size(B, G * Hkv, Hkv, 64, tiles * 32)
-    ctas = min(444, -(-(tiles + 12) * B * Hkv // 4))
-    assert got >= ctas * 2 * G * (64 + 1) * 4 + B * Hkv * 8
+    share = -(-G // 16)
+    runs = min(444 // share, -(-(tiles + 12) * B * Hkv // 4))
+    assert got >= runs * share * 2 * -(-G // share) * (64 + 1) * 4 + B * Hkv * share * 8
     rng = random.Random(tiles + B)
     for _ in range(20):
         n = [rng.choice([0, 1, tiles, rng.randint(0, tiles)]) for _ in range(min(B, 40)) for _ in range(Hkv)]
