@@ -141,12 +141,12 @@ def test_workspace_sizes(gqa_lib):
 @pytest.mark.parametrize("tiles", [1, 4, 5, 33, 1000, 16384])
 def test_workspace_covers_every_cut(gqa_lib, B, Hkv, G, tiles):
     # the units (sequence, head), 12 empty places and their tiles each, in equal runs of
-    # at least 4 places: each CTA writes at most two pieces of its rows.  At most 444 CTAs,
-    # 16 heads in each, so that those of a larger group share a run
+    # at least 4 places, one per CTA or, for more than 16 heads, per two that share them, at
+    # most 444 CTAs: each writes at most two pieces of its rows
     got = b.gqa_decode8_workspace_size(B, G * Hkv, Hkv, 64, tiles * 32)
     share = -(-G // 16)
-    runs = min(444 // share, -(-(tiles + 12) * B * Hkv // 4))
-    assert got >= runs * share * 2 * -(-G // share) * (64 + 1) * 4 + B * Hkv * share * 8
+    ctas = min(444 // share, -(-(tiles + 12) * B * Hkv // 4))    # of one share of the heads
+    assert got >= ctas * share * 2 * -(-G // share) * (64 + 1) * 4 + B * Hkv * share * 8
     rng = random.Random(tiles + B)
     for _ in range(20):
         n = [rng.choice([0, 1, tiles, rng.randint(0, tiles)]) for _ in range(min(B, 40)) for _ in range(Hkv)]
