@@ -13,8 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -123,14 +122,15 @@ double as_double(PyObject *o) {
     return x;
 }
 
-at::Tensor workspace_of(PyObject *o, size_t need_bytes, int &dev) {
-    if (o != Py_None) return need(o, "workspace", at::kByte, 1, dev);
-    return at::empty({static_cast<int64_t>(need_bytes)},
-                     at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+// torch.empty on device dev, without the dispatcher.
+at::Tensor empty_on(at::IntArrayRef shape, at::ScalarType type, int dev) {
+    return at::Tensor(at::detail::empty_cuda(
+        shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
 }
 
-at::Tensor empty_on(at::IntArrayRef shape, at::ScalarType type, int dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
+at::Tensor workspace_of(PyObject *o, size_t need_bytes, int &dev) {
+    if (o != Py_None) return need(o, "workspace", at::kByte, 1, dev);
+    return empty_on({static_cast<int64_t>(need_bytes)}, at::kByte, dev);
 }
 
 // Runs call(stream) with dev current and the GIL released; raises on a non-zero status.
@@ -185,7 +185,7 @@ PyObject *decode8(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                         : static_cast<float>(as_double(a[4]));
     at::Tensor o;
     if (a[6] == Py_None) {
-        o = at::empty_like(q);
+        o = empty_on(q.sizes(), kBf16, dev);
     } else {
         o = need(a[6], "out", kBf16, 3, dev);
         if (o.sizes() != q.sizes()) raise_shape("out must have q's shape", o);
