@@ -214,6 +214,19 @@ def test_decode_repeats_and_reuses_a_dirty_workspace(gqa_lib):
         gqa.decode8(q, c, t, n, workspace=ws[1:])
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(17, 1, 64), (31, 1, 128), (64, 2, 128), (12, 1, 128), (3, 3, 64)])
+def test_decode_stays_in_its_workspace(gqa_lib, Hq, Hkv, d):
+    # units in many pieces, groups shared by two CTAs; bytes past the workspace stay
+    for lens in ([9000, 3, 0, 700], [1], [33] * 300):
+        rng, p, table = make(13, "int8", Hkv, d, 48, 48, lens)
+        q = bf16(rng, (len(lens), Hq, d))
+        need = gqa.decode8_workspace_size(len(lens), Hq, Hkv, d, len(table[0]) * 48)
+        ws = torch.full((need + 512,), 171, dtype=torch.uint8, device="cuda")
+        o = check_decode(p, table, lens, q, workspace=ws[:need])
+        assert torch.equal(check_decode(p, table, lens, q, rope_theta=None, workspace=ws[:need]), o)
+        assert torch.all(ws[need:] == 171)
+
+
 def test_decode_graphs_that_share_a_workspace(gqa_lib):
     lens = [3000, 100, 0, 1500]
     rng, p, table = make(12, "int8", 2, 128, 64, 64, lens)
