@@ -54,14 +54,17 @@
 // identity.
 //
 // Measured on a B200, 8 K/V heads, d = 128 (share of the 6.47 TB/s copy rate): 64
-// sequences of 1024-8192 keys, groups of 4 or 8: 101 us (95 %); groups of 16: 106 us
-// (90 %); groups of 32: 184 us (51 %, bound by the products: two CTAs convert each tile);
+// sequences of 1024-8192 keys, groups of 4 or 8: 103 us (93 %); groups of 16: 107 us
+// (89 %); groups of 32: 184 us (51 %, bound by the products: two CTAs convert each tile);
 // a 2048-key window, int8: 51 us (79 %); two sequences of 100000-131072, groups of
-// 8: 80 us (83 %); one sequence of 1024 keys: 7.4 us (bound by latency: three
-// dependent loads, one tile a warp, a merge).  Steps on the way, on the first of
-// these: heads as M rows 176 us; keys as M rows 126; equal runs in place of splits
-// of 1024 keys, seldom-moved reference, loads ahead of the copies 109; no retries at
-// arrival, packed fp32 106; empty places 103; dependent launch 101.
+// 8: 79 us (84 %); one sequence of 1024 keys: 7.2 us (bound by latency: three
+// dependent loads, one tile a warp, a merge).  68 sequences of 512 keys, 32 heads of 64
+// (five units per CTA, bound by what beginning a unit takes): 41.5 us (53 %).  Steps on
+// the way, on the first of these: heads as M rows 176 us; keys as M rows 126; equal runs
+// in place of splits of 1024 keys, seldom-moved reference, loads ahead of the copies 109;
+// no retries at arrival, packed fp32 106; empty places 103-104.  Arrival as one addition
+// with release and acquire, where two fences stood around it: 7.2 us against 7.5 for the
+// one sequence, 79 against 81 for the two, 34.0 against 35.6 for two of 32768.
 #include <atomic>
 #include <chrono>
 #include <climits>
@@ -191,6 +194,14 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const void *tmap, uint32
         " [%0], [%1, {%3, %4}], [%2];"
         ::"r"(dst), "l"(tmap), "r"(bar), "r"(0), "r"(row)
         : "memory");
+}
+
+// Adds to a word in global memory and returns what was there; release and acquire at
+// device scope.
+__device__ __forceinline__ unsigned long long add_acq_rel(unsigned long long *word, unsigned long long x) {
+    unsigned long long was;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(was) : "l"(word), "l"(x) : "memory");
+    return was;
 }
 
 // Transpose of an 8 x 8 matrix of f16 held one pair per lane.
@@ -787,11 +798,10 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         __syncthreads();                            // the piece's rows are written
         const int pieces = cta1 - cta0 + 1;
         if (threadIdx.x == 0) {
-            __threadfence();                        // ... device-wide
-            const bool last = static_cast<int>(atomicAdd(word, 1ull) & 0xFFFFu) + 1 == pieces;
+            // releases the CTA's rows (ordered before by the barrier) and acquires the others'
+            const bool last = static_cast<int>(add_acq_rel(word, 1ull) & 0xFFFFu) + 1 == pieces;
             if (last) *reinterpret_cast<volatile unsigned long long *>(word) = p.call_id << 16;
             merger = last;
-            __threadfence();                        // every piece's rows are visible
         }
         __syncthreads();
         if (!merger) continue;
