@@ -54,8 +54,8 @@
 // identity.
 //
 // Measured on a B200, 8 K/V heads, d = 128 (share of the 6.47 TB/s copy rate): 64
-// sequences of 1024-8192 keys, groups of 4 or 8: 103 us (93 %); groups of 16: 107 us
-// (89 %); groups of 32: 184 us (51 %, bound by the products: two CTAs convert each tile);
+// sequences of 1024-8192 keys, groups of 4 or 8: 103 us (93 %); 64 of 4608, groups of
+// 16: 109 us (86 %), of 32: 184 us (51 %, bound by the products: two CTAs convert each tile);
 // a 2048-key window, int8: 51 us (79 %); two sequences of 100000-131072, groups of
 // 8: 79 us (84 %); one sequence of 1024 keys: 7.2 us (bound by latency: three
 // dependent loads, one tile a warp, a merge).  68 sequences of 512 keys, 32 heads of 64
