@@ -357,6 +357,10 @@ extern "C" int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, f
     if (T < 0 || T > 0x7fffffff - 2 * kC8MaxBlock)
         return set_error(GQA_ERR_INVALID_ARG, "T=%d must be >= 0 and leave room for a block", T);
     if (B == 0 || T == 0) return GQA_OK;
+    const int n_blk = (T + block - 2) / block + 1;  // blocks that T rows can touch
+    if (n_blk > 65535 || B > 65535)
+        return set_error(GQA_ERR_UNSUPPORTED, "cache8_append: T=%d rows in %d blocks or B=%d exceed 65535", T,
+                         n_blk, B);
     if (int rc = check_ptr(k, 16, "k")) return rc;
     if (int rc = check_ptr(v, 16, "v")) return rc;
     if (int rc = check_ptr(table, 4, "table")) return rc;
@@ -377,11 +381,7 @@ extern "C" int gqa_cache8_append(void *k_cache, void *v_cache, float *k_scale, f
     const int most = T < block ? T : block;         // new rows of a unit at most
     const int unit = (most * d / 64 + 31) / 32 * 32;             // whole warps
     const int per_cta = unit >= 256 ? 1 : 256 / unit;
-    const int n_blk = (T + block - 2) / block + 1;  // blocks that T rows can touch
     const int n_x = (2 * Hkv - 1) / per_cta + 1;
-    if (n_blk > 65535 || B > 65535)
-        return set_error(GQA_ERR_UNSUPPORTED, "cache8_append: T=%d rows in %d blocks or B=%d exceed 65535", T,
-                         n_blk, B);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool int8 = kind == GQA_INT8;
     auto kern = d == 128     ? (int8 ? cache8_append_kernel<128, true, 8> : cache8_append_kernel<128, false, 8>)

@@ -88,6 +88,7 @@ def test_copy(gqa_lib, kw, code):
     (append, dict(T=-1), BAD), (append, dict(T=0x7fffffff), BAD), (append, dict(k=FAKE + 8), BAD),
     (append, dict(v=None), BAD), (append, dict(counts=FAKE + 2), BAD), (append, dict(B=0, kc=None), OK),
     (append, dict(T=0, k=None), OK),
+    (append, dict(B=65536), UNS), (append, dict(T=65535 * 32), UNS),
     (read, dict(T=-1), BAD), (read, dict(T=0x7fffffff), BAD), (read, dict(v=FAKE + 4), BAD),
     (read, dict(B=0, kc=None), OK), (read, dict(T=0, k=None), OK)])
 def test_rows(gqa_lib, call, kw, code):

@@ -686,6 +686,25 @@ def test_sequences_that_share_their_pages(gqa_lib):
     assert np.all(np.abs(o.double().cpu().numpy() - want) <= bound)
 
 
+def test_many_sequences(gqa_lib):
+    # the most that one append takes, one row each: the weight of a lone row is 1
+    B = 65535
+    c = gqa.cache8(B, 1, 64, page=16, block=16, dtype=torch.int8)
+    t = torch.randperm(B, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).int().view(B, 1)
+    refs = torch.zeros(B, dtype=torch.int32, device="cuda")
+    v = torch.randint(-127, 128, (B, 1, 1, 64), device="cuda").to(torch.bfloat16)
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    gqa.cache8_append_(c, t, zero, v, v)
+    k2, v2 = gqa.cache8_read(c, t, zero + 1, 1)
+    assert torch.equal(k2, v) and torch.equal(v2, v)
+    o = gqa.decode8(v[:, 0].expand(B, 4, 64).contiguous(), c, t, zero + 1)
+    assert torch.equal(o, v[:, 0].expand(B, 4, 64))
+    t.fill_(-1)
+    gqa.pages_resize_(t, refs, zero + 16, 16)
+    assert torch.equal(t[:, 0], torch.arange(B, device="cuda").int()) and torch.all(refs == 1)
+    gqa.device_status()
+
+
 def test_large_offsets(gqa_lib):
     # pages past 2^32 bytes of the pool: 36000 pages of 128 KB
     need = 36000 * 8 * 128 * 128 * 2
