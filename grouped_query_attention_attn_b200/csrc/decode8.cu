@@ -40,8 +40,10 @@
 // seen by the warp.  A block whose scale lies in [vref / 64, vref] multiplies
 // its weights by scale / vref before they are rounded to f16 (they keep full
 // precision down to 2^-8); any other scale becomes the new vref and O is
-// rescaled, as for a new maximum.  vref never falls by more than 2^64 at once,
-// which keeps O finite; weights of a smaller block are below 2^-64 vref.
+// rescaled, as for a new maximum.  A vref that falls multiplies O, so it falls no
+// further than leaves the largest element of O at 2^110: however often the scales
+// fall, and whatever follows (at most 2^17 a key), O stays finite.  A fall cut
+// short only loses blocks some 2^80 below what O, of any head, already holds.
 //
 // Groups of 17-32 heads are shared by two CTAs (blockIdx.y), which read the same run at
 // the same time, once from HBM and once from L2.  With all 32 heads in one CTA the
@@ -87,6 +89,8 @@ constexpr int kD8MaxCtas = 148 * kD8CtasPerSm;     // all resident
 constexpr int kD8Heads = 16;                       // query heads of a CTA at most
 constexpr float kD8Least = -3.0e38f;               // reference of a row that has seen no key
 constexpr float kD8Rescale = 8.0f;                 // log2 units: weights stay below 2^8
+constexpr float kD8Room = 0x1p110f;                // a smaller vref makes O no larger than this
+constexpr float kD8HalfTop = 0x1p21f;              // > 16 keys x 2^8 x 448, what half a tile adds
 
 struct D8Params {
     const __nv_bfloat16 *q;
@@ -209,6 +213,20 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+// Largest finite magnitude in a warp's accumulators.
+template <int NT, int N>
+__device__ __forceinline__ float largest(const float (&acc)[NT][N][4]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (fabsf(acc[nt][j][e]) < INFINITY) top = fmaxf(top, fabsf(acc[nt][j][e]));
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
 // NT: tiles of 8 query heads.  kRope: the query is rotated as it is loaded.
@@ -596,10 +614,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     pscale[x] = 0.0f;               // scale 0, or not there
                     if (v == 0.0f || vs[x] == -INFINITY) continue;
                     if (!(v <= vref && v * 64.0f >= vref)) {
-                        const float nv = fmaxf(v, vref * 5.42101086e-20f);          // 2^-64
-                        if (vref > 0.0f) ratio[x] = vref / nv;
-                        vref = nv;
-                        vinv = 1.0f / nv;
+                        if (v < vref) {             // a smaller unit, as far as O has room
+                            float top = largest(oacc);
+                            if (x == 1) top = top * ratio[0] + kD8HalfTop;
+                            ratio[x] = fminf(vref / v, fmaxf(kD8Room / fmaxf(top, kD8Room * 0x1p-126f), 1.0f));
+                            vref /= ratio[x];
+                        } else {
+                            if (vref > 0.0f) ratio[x] = vref / v;
+                            vref = v;
+                        }
+                        vinv = 1.0f / vref;
                     }
                     pscale[x] = v * vinv;
                 }

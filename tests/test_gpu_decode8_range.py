@@ -1,0 +1,74 @@
+"""decode8 over the whole range of V scales that the cache may hold (0 or >= 2^-126), with
+scales that fall far and more than once within the keys of one warp."""
+
+import numpy as np
+import pytest
+import torch
+
+import grouped_query_attention_attn_b200 as gqa
+from oracle import cache8 as oc
+from test_gpu_cache8 import KINDS, bf16, ints, make, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+# exponent of the V scale of a sequence's i-th block of 16 keys
+PATTERNS = {
+    "then_least": lambda i, n: 0 if i < n // 2 else -126,
+    "one_block": lambda i, n: -126 if i // 2 == n // 4 else -5,
+    "halves": lambda i, n: (0, -70)[i % 2],
+    "steps": lambda i, n: (-7, -70, -126)[3 * i // n],
+    "every_tile": lambda i, n: (-7, -71, -126, -7)[i // 2 % 4],
+    "stairs": lambda i, n: 100 - 226 * i // n,
+    "up_and_down": lambda i, n: (-126, 0, -126, 60, -40, -126)[6 * i // n],
+    "zeros_between": lambda i, n: (-3, None, -126)[i % 3],
+}
+
+
+def set_scales(p, table, lens, pattern):
+    for row, n in zip(table, lens):
+        blocks = -(-n // p["block"])
+        per = p["page"] // p["block"]
+        for i in range(blocks):
+            e = PATTERNS[pattern](i, blocks)
+            p["v_scale"][row[i // per], :, i % per] = 0.0 if e is None else 2.0 ** e
+
+
+def check_many(p, table, lens, q, want=None):
+    """The sequences, 27 times over so that every warp takes several tiles of a unit."""
+    n, d = 27, q.shape[-1]
+    o = gqa.decode8(q.repeat(n, 1, 1).cuda(), to_gpu(p), ints(table * n), ints(lens * n))
+    gqa.device_status()
+    want, bound = want or oc.decode(p, table, lens, q.double().numpy(), d ** -0.5)
+    off = np.abs(o.double().cpu().numpy().reshape(n, *want.shape) - want)
+    assert np.all(off <= bound), np.nanmax(off / bound)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("pattern", PATTERNS)
+@pytest.mark.parametrize("G,d", [(2, 128), (9, 128), (2, 64), (9, 64)])
+def test_v_scales_that_fall(gqa_lib, kind, pattern, G, d):
+    lens = [700, 550, 401]
+    rng, p, table = make(len(pattern) + d, kind, 4, d, 32, 16, lens)
+    set_scales(p, table, lens, pattern)
+    check_many(p, table, lens, bf16(rng, (3, 4 * G, d)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_all_the_weight_on_small_values(gqa_lib, kind, d):
+    # the keys of the second half, with V 2^-60 times the first's, take all the weight:
+    # the output is theirs, to its own precision
+    lens = [512, 512, 384]
+    rng, p, table = make(3, kind, 4, d, 32, 16, lens)
+    for row, n in zip(table, lens):
+        for i in range(n // 16):
+            late = i >= n // 32
+            p["v_scale"][row[i // 2], :, i % 2] = 2.0 ** (-60 if late else 0)
+            p["k_scale"][row[i // 2], :, i % 2] = 2.0 ** (0 if late else -126)
+    # keys of one sign, so that the late ones score 130 and more and the others 0: these
+    # have weights below 2^-186, nothing even against values 2^-60 of theirs
+    k = np.minimum(np.ceil(np.abs(oc.values(p["k"], kind))), 32.0) + 32.0
+    p["k"][:] = oc.encode(k, kind)
+    q = torch.full((3, 8, d), 0.5).to(torch.bfloat16)
+    late = [row[n // 64:] for row, n in zip(table, lens)]
+    check_many(p, table, lens, q, oc.decode(p, late, [n // 2 for n in lens], q.double().numpy(), d ** -0.5))
