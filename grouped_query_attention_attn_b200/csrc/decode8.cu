@@ -843,7 +843,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             float4 acc[kR];
 #pragma unroll
             for (int y = 0; y < kR; ++y) {
-                M[y] = -INFINITY;
+                M[y] = kD8Least;                    // finite: a piece of lse NaN has weight NaN
                 wsum[y] = 0.0f;
                 acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
@@ -867,7 +867,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
                     for (int x = 0; x < kBatch; ++x) m = fmaxf(m, l[y][x]);
                     if constexpr (kSub == 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    if (m == -INFINITY) continue;   // no key in any piece so far
                     const float f = fast_exp2(M[y] - m);
                     M[y] = m;
                     wsum[y] *= f;

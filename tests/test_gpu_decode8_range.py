@@ -72,3 +72,22 @@ def test_all_the_weight_on_small_values(gqa_lib, kind, d):
     q = torch.full((3, 8, d), 0.5).to(torch.bfloat16)
     late = [row[n // 64:] for row, n in zip(table, lens)]
     check_many(p, table, lens, q, oc.decode(p, late, [n // 2 for n in lens], q.double().numpy(), d ** -0.5))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [20, 600, 9000])
+def test_nan_stays_nan_in_one_piece_and_in_many(gqa_lib, d, n):
+    # a query with a NaN, and keys of which every group has one: the rows they reach are
+    # NaN, whether their sequence is read by one CTA or cut into pieces; the others stand
+    rng, p, table = make(n + d, "e4m3", 2, d, 32, 16, [n, n])
+    q = bf16(rng, (2, 8, d))
+    q[0, 3, 5] = float("nan")
+    want, bound = oc.decode(p, table, [n, n], q.nan_to_num(0.0).double().numpy(), d ** -0.5)
+    for e in table[1]:
+        p["k"][e, 1, ::7, 9] = 127
+    o = gqa.decode8(q.cuda(), to_gpu(p), ints(table), ints([n, n])).double().cpu().numpy()
+    gqa.device_status()
+    nan = np.zeros(o.shape, bool)
+    nan[0, 3] = nan[1, 4:] = True
+    assert np.array_equal(np.isnan(o), nan)
+    assert np.all(np.abs(o - want)[~nan] <= bound[~nan])
