@@ -34,15 +34,18 @@
 //     paired by byte permutes before the conversion.  P^T is S^T transposed by
 //     movmatrix, 8 x 8 f16 at a time.
 // The running maximum, sums and O stay in fp32; the weights enter the second
-// product in f16 (11 significant bits, at most 2^-12 off).
+// product in f16: 11 significant bits, at most 2^-11 off, from 2^-14 up, and at
+// most 2^-25 off below.  They are held, in the sums too, as 2^7 times themselves:
+// the reference of a score is passed by less than 2^8, so that they fill f16's
+// range to 2^15, and a weight keeps its precision down to 2^-21 of the largest.
 //
 // V scales.  O is kept in units of vref, a running reference of the V scales
 // seen by the warp.  A block whose scale lies in [vref / 64, vref] multiplies
 // its weights by scale / vref before they are rounded to f16 (they keep full
-// precision down to 2^-8); any other scale becomes the new vref and O is
+// precision down to 2^-15 of the largest); any other scale becomes the new vref and O is
 // rescaled, as for a new maximum.  A vref that falls multiplies O, so it falls no
 // further than leaves the largest element of O at 2^110: however often the scales
-// fall, and whatever follows (at most 2^17 a key), O stays finite.  A fall cut
+// fall, and whatever follows (at most 2^24 a key), O stays finite.  A fall cut
 // short only loses blocks some 2^80 below what O, of any head, already holds.
 //
 // Groups of 17-32 heads are shared by two CTAs (blockIdx.y), which read the same run at
@@ -88,9 +91,10 @@ constexpr int kD8CtasPerSm = 3;                    // what shared memory and reg
 constexpr int kD8MaxCtas = 148 * kD8CtasPerSm;     // all resident
 constexpr int kD8Heads = 16;                       // query heads of a CTA at most
 constexpr float kD8Least = -3.0e38f;               // reference of a row that has seen no key
-constexpr float kD8Rescale = 8.0f;                 // log2 units: weights stay below 2^8
+constexpr float kD8Rescale = 8.0f;                 // log2 units: how far a score may pass the reference
+constexpr float kD8Lift = 7.0f;                    // weights in units of 2^-7: below 2^15, f16 holds 2^16
 constexpr float kD8Room = 0x1p110f;                // a smaller vref makes O no larger than this
-constexpr float kD8HalfTop = 0x1p21f;              // > 16 keys x 2^8 x 448, what half a tile adds
+constexpr float kD8HalfTop = 0x1p28f;              // > 16 keys x 2^15 x 448, what half a tile adds
 
 struct D8Params {
     const __nv_bfloat16 *q;
@@ -682,7 +686,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     l_run[nt] = mul2(l_run[nt], alpha);
                     rescale(nt, alpha.x, alpha.y);
                 }
-                const float2 minus_m = make_float2(-m_ref[nt].x, -m_ref[nt].y);
+                const float2 minus_m = make_float2(kD8Lift - m_ref[nt].x, kD8Lift - m_ref[nt].y);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll

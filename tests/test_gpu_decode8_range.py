@@ -91,3 +91,25 @@ def test_nan_stays_nan_in_one_piece_and_in_many(gqa_lib, d, n):
     nan[0, 3] = nan[1, 4:] = True
     assert np.array_equal(np.isnan(o), nan)
     assert np.all(np.abs(o - want)[~nan] <= bound[~nan])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,d", [(2, 128), (9, 128), (2, 64), (9, 64)])
+def test_small_weights_keep_their_precision(gqa_lib, kind, G, d):
+    # of 32 keys one has weight 1 and V = 0, and 16 have weight 2^-14.7 and all of V, in a
+    # block whose V scale is 64 times smaller.  Their weights are within half a step of
+    # f16, 2^-11, and what their scores are off, 2^-20 of 14.7; then bf16's half step 2^-8
+    n, turn = 640, 0.98046875                             # the query, in bf16; log2 units
+    p = oc.pool(n // 32, 1, 32, d, 16, kind)
+    p["k"][:, 0, :, 0] = oc.encode(-15.0, kind)
+    p["k"][:, 0, 0, 0] = oc.encode(0.0, kind)
+    p["v"][:, 0, 16:] = oc.encode(96.0, kind)
+    p["k_scale"][:] = 1.0
+    p["v_scale"][:] = [1.0, 2.0 ** -6]
+    q = torch.zeros((40, G, d), dtype=torch.bfloat16)
+    q[..., 0] = turn
+    o = gqa.decode8(q.cuda(), to_gpu(p), ints([list(range(n // 32))] * 40), ints([n] * 40), scale=float(np.log(2.0)))
+    gqa.device_status()
+    w = 2.0 ** (-15 * turn)
+    want = 16 * w * 96 * 2.0 ** -6 / (1 + 31 * w)
+    assert np.max(np.abs(o.double().cpu().numpy() / want - 1)) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16
