@@ -302,13 +302,11 @@ dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 __syncwarp();
             }
             // copies still in flight land before the block exits
-            mbar_wait(kv_full, 0, abort_flag, p.status, 1000000ull);
+            mbar_drain(kv_full, 0, p.status);
             for (int it = max(0, issued_q - kTcQStages); it < issued_q; ++it)
-                mbar_wait(&q_full[it % kTcQStages], (it / kTcQStages) & 1, abort_flag, p.status,
-                          1000000ull);
+                mbar_drain(&q_full[it % kTcQStages], (it / kTcQStages) & 1, p.status);
             for (int it = max(0, issued_o - kTcOStages); it < issued_o; ++it)
-                mbar_wait(&o_full[it % kTcOStages], (it / kTcOStages) & 1, abort_flag, p.status,
-                          1000000ull);
+                mbar_drain(&o_full[it % kTcOStages], (it / kTcOStages) & 1, p.status);
         }
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ----
@@ -390,7 +388,7 @@ dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if (leader) tc_commit(acc_done);
             __syncwarp();
-            mbar_wait(acc_done, 0, abort_flag, p.status, 1000000000ull);
+            mbar_drain(acc_done, 0, p.status, kWaitLimitNs);
         }
         __syncwarp();
     }
@@ -771,10 +769,9 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             }
         }
         // copies still in flight land before the block exits
-        if (qi > 0) mbar_wait(&qo_full, (qi - 1) & 1, &abort_flag, p.status, 1000000ull);
+        if (qi > 0) mbar_drain(&qo_full, (qi - 1) & 1, p.status);
         for (uint32_t c = kc > kDqKStages ? kc - kDqKStages : 0; c < kc; ++c)
-            mbar_wait(&k_full[c % kDqKStages], (c / kDqKStages) & 1, &abort_flag, p.status,
-                      1000000ull);
+            mbar_drain(&k_full[c % kDqKStages], (c / kDqKStages) & 1, p.status);
     } else if (warp == 2 && lane == 0) {
         // ------------------------------------------------ V ring producer ----
         tma_prefetch_desc(&tm_v);
@@ -797,8 +794,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             }
         }
         for (uint32_t c = vc > kDqVStages ? vc - kDqVStages : 0; c < vc; ++c)
-            mbar_wait(&v_full[c % kDqVStages], (c / kDqVStages) & 1, &abort_flag, p.status,
-                      1000000ull);
+            mbar_drain(&v_full[c % kDqVStages], (c / kDqVStages) & 1, p.status);
     } else if (warp == 1 || warp == 3) {
         // ------------------------------------------------ MMA issuers ----
         // Warp 1 issues S and dP, warp 3 issues dQ.  The two streams touch
@@ -895,7 +891,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         uint64_t *dr = &drain[warp == 1 ? 0 : 1];
         if (leader) tc_commit(dr);
         __syncwarp();
-        mbar_wait(dr, 0, &abort_flag, p.status, 1000000000ull);
+        mbar_drain(dr, 0, p.status, kWaitLimitNs);
     } else if (warp >= 4) {
         // ---------------------------------------- elementwise + epilogue ----
         const int u = (warp - 4) >> 2;                  // key quarter of a tile

@@ -745,7 +745,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // after a time-out, the copies in flight land before the block exits
         if (!ok)
             for (int u = t; u < min(n_iter, t + kStages); ++u) {
-                mbar_wait(&full_bar[warp][st], ph, &abort_flag[warp], p.status, 1000000ull);
+                mbar_drain(&full_bar[warp][st], ph, p.status);
                 if (++st == kStages) {
                     st = 0;
                     ph ^= 1;

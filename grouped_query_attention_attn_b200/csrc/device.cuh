@@ -26,6 +26,7 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // Every wait on a barrier or flag gives up after this long and records
 // GQA_ERR_TIMEOUT; no wait in the library can spin forever.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;   // 1 s
+constexpr uint64_t kDrainLimitNs = 1000ull * 1000ull;            // 1 ms
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -81,6 +82,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
             }
         }
     }
+}
+
+// After a wait has given up: waits for what this block still has in flight (copies into its
+// shared memory, products) before it exits, whatever *abort says, for at most `limit_ns`.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, int *status,
+                                           uint64_t limit_ns = kDrainLimitNs) {
+    const uint32_t addr = smem_u32(bar);
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        if (mbar_try_wait(addr, parity)) return true;
+    } while (globaltimer_ns() - t0 <= limit_ns);
+    record_status(status, GQA_ERR_TIMEOUT);
+    return false;
 }
 
 // ------------------------------------------------------------------- TMA --

@@ -92,18 +92,30 @@ int launch_fold_kv(const void *in, void *out, int B, int T, int H, int g, int d,
     return check_cuda(cudaGetLastError(), "fold_kv_kernel launch");
 }
 
-// One warp waits on a barrier that nothing arrives at; the bounded wait must
-// give up after limit_ns and record GQA_ERR_TIMEOUT in *status.
+// Warp 0 waits on a barrier that nothing arrives at; the bounded wait must
+// give up after limit_ns and record GQA_ERR_TIMEOUT in *status.  It then drains
+// another barrier, as kernels do with their copies in flight, at which warp 1
+// arrives limit_ns / 2 after the wait gave up: GQA_ERR_CUDA if it did not see that.
 __global__ void selftest_wait_kernel(uint64_t limit_ns, int *status) {
-    __shared__ uint64_t bar;
+    __shared__ uint64_t bar[2];
     __shared__ int abort_flag;
     if (threadIdx.x == 0) {
-        mbar_init(&bar, 1);
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
         abort_flag = 0;
         fence_mbar_init();
     }
-    __syncwarp();
-    mbar_wait(&bar, 0, &abort_flag, status, limit_ns);
+    __syncthreads();
+    if (threadIdx.x >= 32) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!*static_cast<volatile int *>(&abort_flag) && globaltimer_ns() - t0 <= 2 * limit_ns) {}
+        const uint64_t t1 = globaltimer_ns();
+        while (globaltimer_ns() - t1 <= limit_ns / 2) {}
+        if (threadIdx.x == 32) mbar_arrive(&bar[1]);
+        return;
+    }
+    mbar_wait(&bar[0], 0, &abort_flag, status, limit_ns);
+    if (!mbar_drain(&bar[1], 0, status, 4 * limit_ns) && threadIdx.x == 0) atomicExch(status, GQA_ERR_CUDA);
 }
 
 // Launches the self-test and waits for it.  The caller reads the status word.
@@ -111,7 +123,7 @@ int selftest_wait_timeout(int timeout_us) {
     int *status = device_status_ptr();
     if (!status) return GQA_ERR_CUDA;
     if (int rc = check_cuda(cudaMemset(status, 0, sizeof(int)), "cudaMemset")) return rc;
-    selftest_wait_kernel<<<1, 32>>>(static_cast<uint64_t>(timeout_us) * 1000ull, status);
+    selftest_wait_kernel<<<1, 64>>>(static_cast<uint64_t>(timeout_us) * 1000ull, status);
     if (int rc = check_cuda(cudaGetLastError(), "selftest_wait_kernel launch")) return rc;
     return check_cuda(cudaDeviceSynchronize(), "selftest sync");
 }

@@ -275,12 +275,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int g = max(0, gi - kPfStages); g < gi; ++g) {
                 const int st = g % kPfStages;
                 const uint32_t ph = (g / kPfStages) & 1;
-                mbar_wait(&k_full[st], ph, &abort_flag, p.status, 1000000ull);
-                mbar_wait(&v_full[st], ph, &abort_flag, p.status, 1000000ull);
+                mbar_drain(&k_full[st], ph, p.status);
+                mbar_drain(&v_full[st], ph, p.status);
             }
             if (ui > 0)
                 for (int k = 0; k < 2; ++k)
-                    mbar_wait(&q_full[k], (ui - 1) & 1, &abort_flag, p.status, 1000000ull);
+                    mbar_drain(&q_full[k], (ui - 1) & 1, p.status);
         }
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ----
@@ -407,7 +407,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         // every MMA this warp issued has finished before tensor memory is freed
         commit(&mma_drain);
-        mbar_wait(&mma_drain, 0, &abort_flag, p.status, 1000000000ull);
+        mbar_drain(&mma_drain, 0, p.status, kWaitLimitNs);
     }
     } else {
         regs_inc<kPfRegsSoftmax>();      // marks the softmax code's budget for the compiler

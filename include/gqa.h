@@ -499,10 +499,13 @@ const char *gqa_last_error(void);
 int gqa_device_status(int reset);
 
 /*
- * gqa_selftest_wait_timeout -- launches a one-warp kernel that waits on a
+ * gqa_selftest_wait_timeout -- launches a small kernel that waits on a
  * shared-memory barrier nothing will ever arrive at, bounded by timeout_us
  * microseconds, and returns what that kernel recorded: GQA_ERR_TIMEOUT when
- * the bound works.  Exercises the failure path of every bounded wait without
+ * the bound works.  A kernel that has given up still waits for its copies and
+ * products in flight before it exits: the kernel then does so on a barrier that
+ * is completed timeout_us / 2 later, and GQA_ERR_CUDA is returned if it leaves
+ * before that.  Exercises the failure path of every bounded wait without
  * hanging or faulting the GPU; synchronises the device; resets the record.
  */
 int gqa_selftest_wait_timeout(int timeout_us);
