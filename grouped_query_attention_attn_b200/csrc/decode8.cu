@@ -77,13 +77,12 @@
 #include <type_traits>
 
 #include "cache8.cuh"
+#include "decode8_runs.cuh"
 
 namespace gqa {
 
-constexpr int kD8Keys = 32;                        // keys per tile
 constexpr int kD8Warps = 4;                        // each takes every fourth tile of a piece
 constexpr int kD8Threads = kD8Warps * 32;
-constexpr int kD8Begin = 12;                       // what beginning a unit costs, in tiles
 constexpr int kD8Epoch = 16;                       // tiles whose pages a warp's lanes hold
 constexpr int kD8MinTiles = kD8Warps;              // shortest run of a CTA
 constexpr float kD8Merge = 0.25f;                  // merging a piece, in tiles of a run
@@ -130,23 +129,6 @@ struct D8Layout {
     static constexpr int kBytes =
         kD8Warps * kRingBytes > kMergeBytes ? kD8Warps * kRingBytes : kMergeBytes;
     static constexpr int kSmemBytes = kBytes + 1024;        // + alignment slack
-};
-
-// Tiles a sequence of L keys reads, in order: those of the sinks
-// below the window, then those from the window's first key on.
-struct D8Tiles {
-    int lo, sinks;              // key j is visible iff j < L and (j >= lo or j < sinks)
-    int n_sink, first, n;       // sink tiles, first window tile, tiles in all
-    __host__ __device__ D8Tiles(int L, int window, int n_sinks) {
-        lo = window > 0 && L > window ? L - window : 0;
-        sinks = window > 0 ? n_sinks : 0;
-        const int below = sinks < lo ? sinks : lo;
-        n_sink = (below + kD8Keys - 1) / kD8Keys;
-        first = lo / kD8Keys > n_sink ? lo / kD8Keys : n_sink;
-        const int last = L / kD8Keys + (L % kD8Keys > 0);
-        n = n_sink + (last > first ? last - first : 0);
-    }
-    __device__ int tile(int i) const { return i < n_sink ? i : first + (i - n_sink); }
 };
 
 // Byte offset of 16-byte chunk c (of D / 16) of key row `key` in a stage tile:
@@ -204,13 +186,18 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const void *tmap, uint32
         : "memory");
 }
 
-// Adds to a word in global memory and returns what was there; release and acquire at
-// device scope.
-__device__ __forceinline__ unsigned long long add_acq_rel(unsigned long long *word, unsigned long long x) {
-    unsigned long long was;
-    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(was) : "l"(word), "l"(x) : "memory");
-    return was;
-}
+// A unit's arrival word in global memory.
+struct D8Word {
+    unsigned long long *at;
+    __device__ unsigned long long read() const { return *reinterpret_cast<volatile unsigned long long *>(at); }
+    __device__ void set(unsigned long long x) const { *reinterpret_cast<volatile unsigned long long *>(at) = x; }
+    __device__ void cas(unsigned long long from, unsigned long long to) const { atomicCAS(at, from, to); }
+    __device__ unsigned long long add(unsigned long long x) const {      // release and acquire, device scope
+        unsigned long long was;
+        asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(was) : "l"(at), "l"(x) : "memory");
+        return was;
+    }
+};
 
 // Transpose of an 8 x 8 matrix of f16 held one pair per lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
@@ -274,6 +261,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         return n > 0 ? n + kD8Begin : 0;
     };
 
+    auto word_of = [&](size_t unit) { return D8Word{p.arrivals + unit * gridDim.y + blockIdx.y}; };
+
     // ---- this CTA's run of tiles; every warp finds it for itself ----
     int total = 0, longest = 0;                     // total fits an int (checked on the host)
     for (int b = lane; b < p.B; b += 32) {
@@ -289,11 +278,10 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int least = static_cast<int>(sqrtf(kD8Merge * __reduce_max_sync(0xffffffffu, longest)));
     const int per = max((least + kD8Warps) / kD8Warps * kD8Warps,
                         (total - 1) / static_cast<int>(gridDim.x) + 1);
-    int pos = per * blockIdx.x;
-    const int end = min(pos + per, total);
-    // the unit it begins in: sequence b, K/V head kvh, place of its first tile
-    int b = 0, kvh = 0, tile0 = 0;
-    if (pos < end)
+    D8Run run = {per * static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+    run.end = min(run.pos + per, total);
+    // the unit it begins in
+    if (run.pos < run.end)
         for (int b0 = 0, off = 0; b0 < p.B; b0 += 32) {          // one is found: pos < total
             const int places = b0 + lane < p.B ? places_of(b0 + lane) : 0, n = places * p.Hkv;
             int x = n;                              // inclusive prefix sum
@@ -302,14 +290,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const int y = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += y;
             }
-            const uint32_t past = __ballot_sync(0xffffffffu, pos < off + x);
+            const uint32_t past = __ballot_sync(0xffffffffu, run.pos < off + x);
             if (past) {
                 const int l = __ffs(past) - 1;      // first sequence that ends past pos
                 const int each = __shfl_sync(0xffffffffu, places, l);
-                b = b0 + l;
+                run.b = b0 + l;
                 off += __shfl_sync(0xffffffffu, x - n, l);
-                kvh = (pos - off) / each;
-                tile0 = off + kvh * each + kD8Begin;
+                run.kvh = (run.pos - off) / each;
+                run.tile0 = off + run.kvh * each + kD8Begin;
                 break;
             }
             off += __shfl_sync(0xffffffffu, x, 31);
@@ -333,31 +321,19 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     uint32_t ph = 0;
     // (b < B holds by the sums above; it is checked so that lengths which change under
     // the kernel can end the run early, but not lead it astray)
-    while (pos < end && b < p.B) {
-        const int len = p.seqlens[b], L = min(max(len, 0), Lmax);
+    while (run.pos < run.end && run.b < p.B) {
+        const int b = run.b, len = p.seqlens[b], L = min(max(len, 0), Lmax);
         const D8Tiles seq(L, p.window, p.sinks);
         if (seq.n == 0) {
-            ++b;
+            ++run.b;
             continue;
         }
-        // ---- the piece: tiles first .. first + count - 1 of unit (b, kvh) ----
-        const int head = kvh, unit_end = tile0 + seq.n, stop = min(unit_end, end);
-        const int first = max(pos - tile0, 0), count = stop - (tile0 + first);
-        // CTAs whose runs hold the unit's first and last tile
-        int cta0 = blockIdx.x, cta1 = blockIdx.x;
-        if (first > 0) cta0 = tile0 / per;
-        if (unit_end > end) cta1 = min((unit_end - 1) / per, static_cast<int>(gridDim.x) - 1);
+        const D8Piece piece = d8_take(run, seq.n, p.Hkv, per, blockIdx.x, gridDim.x);
+        const int head = piece.head, first = piece.first, count = piece.count;
+        const int cta0 = piece.cta0, cta1 = piece.cta1;
         const size_t unit = static_cast<size_t>(b) * p.Hkv + head;
         const size_t grow0 = unit * (p.Hq / p.Hkv) + blockIdx.y * p.share;
         const int32_t *row = p.table + static_cast<size_t>(b) * p.M;
-        pos = stop;                                 // (a run may end in the empty places)
-        if (pos == unit_end) {                      // on to the next unit
-            tile0 = unit_end + kD8Begin;
-            if (++kvh == p.Hkv) {
-                kvh = 0;
-                ++b;
-            }
-        }
         if (count <= 0) continue;
         const int n_iter = (count - warp + kD8Warps - 1) / kD8Warps;      // tiles of this warp
         auto key_of = [&](int t) { return seq.tile(first + warp + t * kD8Warps) * kD8Keys; };
@@ -428,13 +404,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
             __syncwarp();
         };
-        // Arrival word of a unit in several pieces: call id in the high 48 bits, arrivals
-        // in the low 16.  Every piece claims the word for this call before it starts
-        // (whatever another call, or uninitialised memory, left there; if the exchange
-        // fails, another piece has claimed it), so that an arrival is one addition.  The
-        // last one leaves (call id, 0) for a replay of the same launch.
-        unsigned long long *word = p.arrivals + unit * gridDim.y + blockIdx.y, left = 0;
-        if (threadIdx.x == 0 && cta0 != cta1) left = *reinterpret_cast<volatile unsigned long long *>(word);
+        const D8Word word = word_of(unit);
+        unsigned long long left = 0;
+        if (threadIdx.x == 0 && cta0 != cta1) left = word.read();
         // Loads that nothing waits for yet come first: once the copies of all CTAs are
         // under way, a load takes several microseconds.
         Group cur, next;
@@ -470,8 +442,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         load_scales(0, cur);
         for (int t = 0; t < min(n_iter, kStages); ++t)
             issue(t, st + t < kStages ? st + t : st + t - kStages, cur.row);
-        if (threadIdx.x == 0 && cta0 != cta1 && (left >> 16) != p.call_id)
-            atomicCAS(word, left, p.call_id << 16);
+        if (threadIdx.x == 0 && cta0 != cta1) d8_claim(word, left, p.call_id);
         if constexpr (kRope) {
             if (turn) __syncthreads();
 #pragma unroll
@@ -762,7 +733,15 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
         vref = fmaxf(vref, 0.0f);
         __syncthreads();                                // every tile consumed: reuse the rings
-        if (abort_flag[0] | abort_flag[1] | abort_flag[2] | abort_flag[3]) return;
+        if (abort_flag[0] | abort_flag[1] | abort_flag[2] | abort_flag[3]) {
+            if (threadIdx.x == 0) {                     // a replay finds the words as it needs them
+                if (cta0 != cta1) d8_arrive(word, cta1 - cta0 + 1, p.call_id);
+                d8_abandon(run, p.B, p.Hkv, per, blockIdx.x, gridDim.x, p.call_id,
+                           [&](int z) { return max(places_of(z) - kD8Begin, 0); },
+                           [&](int z, int h) { return word_of(static_cast<size_t>(z) * p.Hkv + h); });
+            }
+            return;
+        }
         constexpr int kRows = Lay::kRows, kStride = Lay::kRowFloats;
         float *s_o = reinterpret_cast<float *>(smem);             // [warp][row][kStride]
         float *s_m = s_o + kD8Warps * kRows * kStride;            // [warp][row]
@@ -827,9 +806,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int pieces = cta1 - cta0 + 1;
         if (threadIdx.x == 0) {
             // releases the CTA's rows (ordered before by the barrier) and acquires the others'
-            const bool last = static_cast<int>(add_acq_rel(word, 1ull) & 0xFFFFu) + 1 == pieces;
-            if (last) *reinterpret_cast<volatile unsigned long long *>(word) = p.call_id << 16;
-            merger = last;
+            merger = d8_arrive(word, pieces, p.call_id);
         }
         __syncthreads();
         if (!merger) continue;
