@@ -120,13 +120,17 @@ def decode(p, table, lens, q, scale, window=0, sinks=0):
     """q float64 [B, Hq, d] -> (o, bound): o float64 [B, Hq, d] and how far bf16 outputs of
     the kernel's arithmetic may be off, elementwise.
 
-    Bound.  A weight is off by at most 2^-12 (f16), relatively, and by what its
-    score is off: fp32 sums of d products (d 2^-24 of the sum of magnitudes, plus
-    as much again for the operands' scaling and the exponential's 2^-21), and an
-    element of q below 2^-14 of its row's largest value is off by 2^-25 of that.
-    An output, a quotient of two sums, is off by twice the weights' error times
-    sum p |v| / sum p.  Weights under 2^-14 are off by 2^-25 absolutely, in units of
-    a V scale at most 64 times their own.  Then half a step of bf16, 2^-8.
+    Bound, in units of the row's largest weight w = 1, A = sum w |v| / sum w.
+    A score is off by fp32 sums of d products (d 2^-24 of the sum of magnitudes, plus as
+    much again for the operands' scaling) and by elements of q below 2^-14 of their row's
+    largest value, off by 2^-25 of that; a weight by as much and the exponential's
+    2^-21, in the numerator and in the sum: twice that of A.  In the numerator only, a
+    weight is rounded to f16, by 2^-11 of itself; and fp32 sums of up to 512 terms (a
+    warp's products, then its pieces) add 2^-15.  Weights enter as 2^7 times themselves,
+    times their V scale over a reference at most 64 times that: below w = 2^-15 they may be
+    under f16's 2^-14 and off by 2^-25 absolutely, 2^-26 of |v| each.  A block whose V scale
+    lies more than 2^80 below the sequence's largest may be lost.  Then half a step of
+    bf16, 2^-8.
     """
     B, Hq, d = q.shape
     H = p["k"].shape[1]
@@ -145,10 +149,12 @@ def decode(p, table, lens, q, scale, window=0, sinks=0):
             w = np.exp(s - s.max())
             o[b, h] = w @ v / w.sum()
             mag = (np.abs(k) @ np.abs(q[b, h]) * scale).max()
-            off = 2.0 * d * 2.0 ** -24 * mag + 2.0 ** -21 + 2.0 ** -12
+            off = 2.0 * d * 2.0 ** -24 * mag + 2.0 ** -21
             off += 2.0 ** -25 * np.abs(q[b, h]).max() * np.abs(k).sum(1).max() * scale
-            small = len(k) * 2.0 ** -25 * 64 * np.abs(v).max()
-            bound[b, h] += 2.0 ** -8 * np.abs(o[b, h]) + 2 * off * (w @ np.abs(v)) / w.sum() + small
+            av = np.abs(v)
+            mean = w @ av / w.sum()
+            small = 2.0 ** -26 * av[w < 2.0 ** -15].sum(0) / w.sum() + 2.0 ** -80 * av.max()
+            bound[b, h] += 2.0 ** -8 * np.abs(o[b, h]) + (2 * off + 2.0 ** -11 + 2.0 ** -15) * mean + small
     return o, bound
 
 

@@ -7,7 +7,8 @@ import torch
 
 import grouped_query_attention_attn_b200 as gqa
 from oracle import cache8 as oc
-from test_gpu_cache8 import KINDS, bf16, ints, make, to_gpu
+from test_gpu_cache8 import KINDS, bf16, check_decode, ints, make, to_gpu
+from test_oracle_cache8_bound import case as long_case
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,16 @@ def test_small_weights_keep_their_precision(gqa_lib, kind, G, d):
     w = 2.0 ** (-15 * turn)
     want = 16 * w * 96 * 2.0 ** -6 / (1 + 31 * w)
     assert np.max(np.abs(o.double().cpu().numpy() / want - 1)) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16
+
+
+@pytest.mark.parametrize("G", [1, 6, 20])
+@pytest.mark.parametrize("n,d", [(9000, 128), (20000, 64), (40000, 64)])
+def test_pieces_whose_values_differ(gqa_lib, n, d, G):
+    # every page has V of its own: a page lost or read twice is at least twice the bound
+    # (test_oracle_cache8_bound)
+    p, pages, q = long_case(n, d, n + 1, True)
+    rng = np.random.default_rng(G)
+    q = np.concatenate([q] + [np.round(rng.standard_normal((1, 1, d)) * 64) / 64 for _ in range(G - 1)], 1)
+    q = torch.from_numpy(q).to(torch.bfloat16)
+    for lens in ([n], [n, 100, n - 7]):
+        check_decode(p, [pages] * len(lens), lens, q.repeat(len(lens), 1, 1))
