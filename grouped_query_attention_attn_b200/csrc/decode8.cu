@@ -91,6 +91,7 @@ constexpr int kD8MaxCtas = 148 * kD8CtasPerSm;     // all resident
 constexpr int kD8Heads = 16;                       // query heads of a CTA at most
 constexpr float kD8Least = -3.0e38f;               // reference of a row that has seen no key
 constexpr float kD8Rescale = 8.0f;                 // log2 units: how far a score may pass the reference
+constexpr float kD8Pieces = 10.0f;                 // pieces weigh at most 2^-10: a unit has fewer than 2^10
 constexpr float kD8Lift = 7.0f;                    // weights in units of 2^-7: below 2^15, f16 holds 2^16
 constexpr float kD8Room = 0x1p110f;                // a smaller vref makes O no larger than this
 constexpr float kD8HalfTop = 0x1p28f;              // > 16 keys x 2^15 x 448, what half a tile adds
@@ -232,6 +233,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     constexpr int kStages = Lay::kStages;
     __shared__ uint64_t full_bar[kD8Warps][kStages];
     __shared__ int abort_flag[kD8Warps], merger;
+    __shared__ __align__(16) float s_vref[kD8Warps];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;        // quad, lane in quad
@@ -731,7 +733,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 l_run[nt].x += __shfl_xor_sync(0xffffffffu, l_run[nt].x, x);
                 l_run[nt].y += __shfl_xor_sync(0xffffffffu, l_run[nt].y, x);
             }
-        vref = fmaxf(vref, 0.0f);
+        if (lane == 0) s_vref[warp] = fmaxf(vref, 0.0f);
         __syncthreads();                                // every tile consumed: reuse the rings
         if (abort_flag[0] | abort_flag[1] | abort_flag[2] | abort_flag[3]) {
             if (threadIdx.x == 0) {                     // a replay finds the words as it needs them
@@ -747,6 +749,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         float *s_m = s_o + kD8Warps * kRows * kStride;            // [warp][row]
         float *s_l = s_m + kD8Warps * kRows;                      // [warp][row]
         auto column = [](int c) { return c + 4 * (c / (D / 8)); };
+        // Sums of large values may be past fp32's range although their mean is not, so the
+        // rows stay in units of their warp's vref: v_rel takes these to v_unit, a power of two
+        // near the largest, which the mean is multiplied by.
+        const float4 v_of = *reinterpret_cast<const float4 *>(s_vref);
+        const float v_top = fmaxf(fmaxf(v_of.x, v_of.y), fmaxf(v_of.z, v_of.w));
+        const uint32_t v_exp = min(max(__float_as_uint(v_top) >> 23, 1u), 253u);   // unit and inverse are normal
+        const float v_unit = __uint_as_float(v_exp << 23), v_inv = __uint_as_float((254 - v_exp) << 23);
+        const float v_rel[kD8Warps] = {v_of.x * v_inv, v_of.y * v_inv, v_of.z * v_inv, v_of.w * v_inv};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -756,8 +766,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
                 for (int j = 0; j < D / 16; j += 2)
                     *reinterpret_cast<float4 *>(dst + 2 * j) =
-                        make_float4(oacc[nt][j][h] * vref, oacc[nt][j][h + 2] * vref,
-                                    oacc[nt][j + 1][h] * vref, oacc[nt][j + 1][h + 2] * vref);
+                        make_float4(oacc[nt][j][h], oacc[nt][j][h + 2], oacc[nt][j + 1][h], oacc[nt][j + 1][h + 2]);
                 if (gq == 0) {
                     s_m[warp * kRows + r] = h ? m_ref[nt].y : m_ref[nt].x;
                     s_l[warp * kRows + r] = h ? l_run[nt].y : l_run[nt].x;
@@ -776,14 +785,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const float f = fast_exp2(s_m[w * kRows + r] - M);
                 const float4 x =
                     *reinterpret_cast<const float4 *>(s_o + (w * kRows + r) * kStride + column(c));
+                const float g = f * v_rel[w];
                 wsum += f * s_l[w * kRows + r];
-                acc.x += f * x.x;
-                acc.y += f * x.y;
-                acc.z += f * x.z;
-                acc.w += f * x.w;
+                acc.x += g * x.x;
+                acc.y += g * x.y;
+                acc.z += g * x.z;
+                acc.w += g * x.w;
             }
             const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
-            acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            acc = make_float4(acc.x * inv * v_unit, acc.y * inv * v_unit, acc.z * inv * v_unit,
+                              acc.w * inv * v_unit);
             if (cta0 == cta1) {
                 *reinterpret_cast<uint2 *>(p.o + (grow0 + r) * D + c) =
                     make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
@@ -850,6 +861,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     if constexpr (kSub == 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                     const float f = fast_exp2(M[y] - m);
                     M[y] = m;
+                    m += kD8Pieces;
                     wsum[y] *= f;
                     float4 a = make_float4(acc[y].x * f, acc[y].y * f, acc[y].z * f, acc[y].w * f);
 #pragma unroll

@@ -116,6 +116,20 @@ def test_small_weights_keep_their_precision(gqa_lib, kind, G, d):
     assert np.max(np.abs(o.double().cpu().numpy() / want - 1)) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("few", [False, True])
+def test_values_at_the_end_of_the_range(gqa_lib, kind, d, few):
+    # V up to 1.75 x 2^127: any sum of two is past fp32, their means are not.  few: one block
+    # in nine, the others 2^139 below
+    lens = [1, 20, 700, 9000]
+    rng, p, table = make(d + few, kind, 2, d, 32, 16, lens)
+    for row, n in zip(table, lens):
+        for i in range(-(-n // 16)):
+            p["v_scale"][row[i // 2], :, i % 2] = 2.0 ** (-20 if few and i % 9 else 119)
+    check_decode(p, table, lens, bf16(rng, (4, 6, d)))
+
+
 @pytest.mark.parametrize("G", [1, 6, 20])
 @pytest.mark.parametrize("n,d", [(9000, 128), (20000, 64), (40000, 64)])
 def test_pieces_whose_values_differ(gqa_lib, n, d, G):
