@@ -89,15 +89,21 @@ def lib():
 
 def torch_binding():
     """The extension with the tensor-level calls of the paged 8-bit cache (torch_binding.cpp),
-    bound to the library (raises RuntimeError if either is not built)."""
+    bound to the library (raises RuntimeError if either is not built, or the extension
+    was built for another torch or Python)."""
     global _torch
     if _torch is None:
         handle = lib()
+        from . import build
+        run = "run `python -m grouped_query_attention_attn_b200.build`"
+        if not os.path.exists(build.TORCH_BINDING):
+            raise RuntimeError(f"the torch binding is not built: {run}")
+        if not build.torch_binding_fits():
+            raise RuntimeError(f"the torch binding was not built for {build.torch_binding_target()}: {run}")
         try:
             from . import _torch_binding as ext
         except ImportError as e:
-            raise RuntimeError("the torch binding is not built: run `python -m "
-                               "grouped_query_attention_attn_b200.build`") from e
+            raise RuntimeError(f"the torch binding does not load ({e}): {run} --force") from e
         ext.bind(lambda name: ctypes.cast(getattr(handle, name), ctypes.c_void_p).value)
         _torch = ext
     return _torch

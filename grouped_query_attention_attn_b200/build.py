@@ -5,7 +5,8 @@
 Each .cu under csrc/ is compiled to an object in _build/ (in parallel), then
 linked into grouped_query_attention_attn_b200/libgqa.so.  csrc/torch_binding.cpp
 becomes the CPython extension _torch_binding.so (g++, torch's headers).  Objects
-are rebuilt when their source or any header changed.
+are rebuilt when their source or any header changed, the extension also when torch or
+Python did.
 """
 
 import argparse
@@ -13,6 +14,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -50,13 +52,27 @@ def _compile(src, force, verbose, extra):
     return obj, (res.stderr if verbose else "")
 
 
+def torch_binding_target():
+    """The torch and Python whose binary interfaces the torch binding is compiled against."""
+    import torch
+    return (f"torch {torch.__version__}, CXX11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def torch_binding_fits():
+    """Whether the present binding was built for torch_binding_target(): it holds that string."""
+    try:
+        with open(TORCH_BINDING, "rb") as f:
+            return b"<" + torch_binding_target().encode() + b">" in f.read()
+    except OSError:
+        return False
+
+
 def _build_torch_binding(force):
     src = os.path.join(CSRC, "torch_binding.cpp")
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "gqa.h")))
-    if not force and os.path.exists(TORCH_BINDING) and os.path.getmtime(TORCH_BINDING) >= newest:
+    if not force and torch_binding_fits() and os.path.getmtime(TORCH_BINDING) >= newest:
         return
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
@@ -65,7 +81,8 @@ def _build_torch_binding(force):
     tmp = TORCH_BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f"-I{d}" for d in inc), src, "-o", tmp, f"-L{os.path.join(root, 'lib')}",
+           f'-DGQA_BUILT_FOR="<{torch_binding_target()}>"', *(f"-I{d}" for d in inc), src, "-o", tmp,
+           f"-L{os.path.join(root, 'lib')}",
            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -377,4 +377,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_binding() { return PyModule_Create(&module); }
+// built_for: the torch and Python it was compiled against (build.py looks for it in the file)
+PyMODINIT_FUNC PyInit__torch_binding() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", GQA_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
