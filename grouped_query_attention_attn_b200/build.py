@@ -11,7 +11,9 @@ Python did.
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -92,7 +94,8 @@ def _build_torch_binding(force):
 
 def build_library(force=False, verbose=False, extra_flags=()):
     """Compile every CUDA source for sm_100a and link libgqa.so (returns its path), and
-    build the torch binding."""
+    build the torch binding, which needs torch and g++: without either the library is
+    built alone, and what is missing is said on stderr."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = _sources()
     extra = list(extra_flags)
@@ -112,7 +115,12 @@ def build_library(force=False, verbose=False, extra_flags=()):
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB)
-    _build_torch_binding(force)
+    missing = [what for what, there in (("torch", importlib.util.find_spec("torch")), ("g++", shutil.which("g++")))
+               if not there]
+    if missing:
+        sys.stderr.write(f"the torch binding is not built: no {' and no '.join(missing)}\n")
+    else:
+        _build_torch_binding(force)
     return LIB
 
 

@@ -58,3 +58,20 @@ def test_the_reason_of_a_failed_import_is_given(gqa_lib, monkeypatch):
     monkeypatch.setitem(sys.modules, MODULE, None)
     with pytest.raises(RuntimeError, match="does not load .*halted"):
         _binding.torch_binding()
+
+
+@pytest.mark.parametrize("missing", ["torch", "g++"])
+def test_the_library_is_built_without(compiles, monkeypatch, capsys, missing):
+    monkeypatch.setattr(build, "TORCH_BINDING", build.TORCH_BINDING + ".missing")
+    if missing == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+        monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    else:
+        monkeypatch.setattr(build.shutil, "which", lambda name: None)
+        monkeypatch.setattr(build.subprocess, "run", no_such_file)
+    assert build.build_library() == build.LIB
+    assert f"no {missing}" in capsys.readouterr().err and compiles == []
+
+
+def no_such_file(cmd, **kw):
+    raise FileNotFoundError(cmd[0])
