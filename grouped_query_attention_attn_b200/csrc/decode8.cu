@@ -455,7 +455,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 qb[s][1] = rope_rotate_pair(qb[s][1], c1.x, c1.y);
             }
         }
-        // bring the row's largest value into [1, 2); an infinite or zero row stays as it is
+        // bring the row's largest value into [1, 2), a subnormal one near it; an infinite row stays
+        // as it is
         float q_max = 0.0f;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
@@ -465,8 +466,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         q_max = fmaxf(q_max, __shfl_xor_sync(0xffffffffu, q_max, 1));
         q_max = fmaxf(q_max, __shfl_xor_sync(0xffffffffu, q_max, 2));
         const int q_exp = static_cast<int>(__float_as_uint(q_max) >> 23);   // biased exponent
-        const bool fit = q_exp > 0 && q_exp < 255;
-        const uint32_t ex = min(q_exp, 253);            // 2^(ex - 127) and its inverse are normal
+        const bool fit = q_exp < 255;
+        const uint32_t ex = min(max(q_exp, 1), 253);    // 2^(ex - 127) and its inverse are normal
         const float up = fit ? __uint_as_float((254 - ex) << 23) : 1.0f;
         const float down = (fit ? __uint_as_float(ex << 23) : 1.0f) * p.scale_log2;
 #pragma unroll

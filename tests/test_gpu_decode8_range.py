@@ -117,6 +117,18 @@ def test_small_weights_keep_their_precision(gqa_lib, kind, G, d):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,d", [(2, 128), (9, 128), (2, 64), (9, 64)])
+def test_queries_at_the_small_end_of_bf16(gqa_lib, kind, G, d):
+    # the largest element of a row is subnormal, or just normal; scale brings the scores to 1
+    lens = [300, 33]
+    rng, p, table = make(G + d, kind, 2, d, 32, 16, lens)
+    for f, scale in ((2.0 ** -131, 2.0 ** 127), (2.0 ** -126, 2.0 ** 123)):
+        q = (bf16(rng, (2, 2 * G, d)).float().clamp(-3, 3) * f).to(torch.bfloat16)
+        assert int((q != 0).sum()) > q.numel() // 2
+        check_decode(p, table, lens, q, scale=scale)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("few", [False, True])
 def test_values_at_the_end_of_the_range(gqa_lib, kind, d, few):
