@@ -292,6 +292,8 @@ def cache8(n_pages, Hkv, d, page=64, block=64, dtype=torch.float8_e4m3fn, device
     """An empty Cache8 of n_pages pages of ``page`` rows, scales per ``block`` rows."""
     if page < 1 or block < 1 or page % block:
         raise ValueError(f"block={block} must divide page={page}")
+    if dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise ValueError(f"dtype={dtype} must be torch.float8_e4m3fn or torch.int8")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     pool, scale = (n_pages, Hkv, page, d), (n_pages, Hkv, page // block)
     return Cache8(torch.zeros(pool, dtype=torch.uint8, device=dev).view(dtype),
