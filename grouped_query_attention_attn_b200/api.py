@@ -306,8 +306,9 @@ def cache8_append_(cache, table, seqlens, k, v, counts=None):
     """Quantise new rows into a Cache8, in place: the first counts[b] (default T) rows
     of bf16 k, v [B, T, Hkv, d] become rows seqlens[b], seqlens[b] + 1, ... of sequence
     b (table [B, M], seqlens, counts [B] int32; seqlens is not changed).  The scale of a
-    block is the smallest power of two that covers its rows; rows already in a block
-    are requantised when its scale grows.  The page of row seqlens[b] must belong to
+    block is the smallest power of two that covers its rows (int8 loses up to one of its
+    seven bits against max / 127); rows already in a block are requantised, and so
+    rounded again, when its scale grows.  The page of row seqlens[b] must belong to
     sequence b alone.  Returns cache."""
     return _b.torch_binding().cache8_append_(cache, table, seqlens, k, v, counts)
 
@@ -338,9 +339,11 @@ def decode8(q, cache, table, seqlens, scale=None, workspace=None, out=None, wind
     q [B, Hq, d] bf16, table [B, M] and seqlens [B] int32 on the device; returns
     [B, Hq, d].  ``window`` (an int >= 1) leaves the newest ``window`` rows and the first
     ``sinks`` visible.  ``rope_theta`` rotates q as it is loaded (position
-    max(seqlens[b] - 1, 0)); the cached keys must already be rotated.  ``workspace``: a
-    uint8 CUDA tensor of at least decode8_workspace_size(...) bytes (allocated here when
-    None)."""
+    max(seqlens[b] - 1, 0)); the cached keys must already be rotated.  Weights enter the
+    product with V in fp16 (11 bits) and elements of q below 2^-14 of their row's largest
+    count to 2^-25 of it; scores, statistics and sums are fp32.  ``workspace``:
+    a uint8 CUDA tensor of at least decode8_workspace_size(...) bytes (allocated here
+    when None)."""
     return _b.torch_binding().decode8(q, cache, table, seqlens, scale, workspace, out, window, sinks,
                                       rope_theta)
 

@@ -59,12 +59,13 @@
 // identity.
 //
 // Measured on a B200, 8 K/V heads, d = 128 (share of the 6.47 TB/s copy rate): 64
-// sequences of 1024-8192 keys, groups of 4 or 8: 103 us (93 %); 64 of 4608, groups of
-// 16: 109 us (86 %), of 32: 184 us (51 %, bound by the products: two CTAs convert each tile);
-// a 2048-key window, int8: 51 us (79 %); two sequences of 100000-131072, groups of
-// 8: 79 us (84 %); one sequence of 1024 keys: 7.2 us (bound by latency: three
-// dependent loads, one tile a warp, a merge).  68 sequences of 512 keys, 32 heads of 64
-// (five units per CTA, bound by what beginning a unit takes): 41.5 us (53 %).  Steps on
+// sequences of 1024-8192 keys, groups of 4: 103 us (93 %; on other cards up to 112); 64 of
+// 4608, groups of 16: 107 us (88 %), of 32: 184 us (51 %, bound by the products: two CTAs
+// convert each tile); a 2048-key window, int8: 51 us (79 %); two sequences of
+// 100000-131072, groups of 8: 79 us (85 %); one sequence of 1024 keys: 7.3 us (bound by
+// latency: three dependent loads, one tile a warp, a merge).  d = 64: 64 of 4608, groups of 4,
+// 56 us (83 %), 128 of 8192 172 us (97 %); 68 sequences of 512 keys, 32 heads (five units
+// per CTA, bound by what beginning a unit takes) 42.6 us (52 %).  Steps on
 // the way, on the first of these: heads as M rows 176 us; keys as M rows 126; equal runs
 // in place of splits of 1024 keys, seldom-moved reference, loads ahead of the copies 109;
 // no retries at arrival, packed fp32 106; empty places 103-104.  Arrival as one addition
@@ -276,7 +277,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // A unit of n tiles in runs of r has n / r pieces to merge, one after the other, for
     // r tiles read side by side by four warps: runs are not shorter than about
     // sqrt(n kD8Merge), in whole rounds of the warps.  (One unit of 32 heads, d = 64,
-    // 60000 keys: 61 us with runs of 4 tiles at least, 31 so; 1024 keys in 8 units, 7.2.)
+    // 60000 keys: 61 us with runs of 4 tiles at least, 31 so, 22 with the heads shared by two
+    // CTAs since; 1024 keys in 8 units, 7.3.)
     const int least = static_cast<int>(sqrtf(kD8Merge * __reduce_max_sync(0xffffffffu, longest)));
     const int per = max((least + kD8Warps) / kD8Warps * kD8Warps,
                         (total - 1) / static_cast<int>(gridDim.x) + 1);

@@ -430,7 +430,11 @@ size_t gqa_decode8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax);
  * workspace: >= gqa_decode8_workspace_size(B, Hq, Hkv, d, M * page) bytes,
  * 256-byte aligned, contents on entry irrelevant; calls in flight at the same
  * time (other streams, captured graphs) need workspaces of their own.
- * K and V are read once; scores, softmax and output sums are fp32.
+ * K and V are read once; scores, softmax and output sums are fp32 (so a block's
+ * k_scale times scale times the largest |q| of a head stays below 2^127).  Softmax
+ * weights enter the product with V in fp16 (2^-11 off), elements of q below 2^-14 of
+ * their row's largest value are held to 2^-25 of it, and V blocks whose scale is
+ * some 2^80 below that of others of the sequence may count as 0.
  */
 int gqa_decode8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                 const float *v_scale, const int32_t *table, const int32_t *seqlens, void *o, int kind,
