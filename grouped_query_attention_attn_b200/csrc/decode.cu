@@ -20,8 +20,6 @@
 // so the merge of one group overlaps the other groups' streaming and no
 // second kernel waits for the whole grid.
 #include <cuda_bf16.h>
-#include <atomic>
-#include <chrono>
 #include <cmath>
 
 #include "device.cuh"
@@ -459,19 +457,6 @@ struct DecWorkspace {
 
 size_t decode_workspace_bytes(int B, int Hq, int Hkv, int d, int Lmax) {
     return DecWorkspace(B, Hq, Hkv, d, Lmax).bytes;
-}
-
-// Per-call ids for the arrival words: 48 bits, never 0, different for every
-// launch of the process (the start is drawn from the clock, so a workspace
-// reused by another process is unlikely to hold a matching word either).
-static unsigned long long next_call_id() {
-    static std::atomic<unsigned long long> counter{
-        static_cast<unsigned long long>(
-            std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull};
-    for (;;) {
-        const unsigned long long id = counter.fetch_add(1) & 0xFFFFFFFFFFFFull;
-        if (id != 0) return id;
-    }
 }
 
 template <int D, int MB, bool kRope>

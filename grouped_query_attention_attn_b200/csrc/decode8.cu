@@ -71,8 +71,6 @@
 // no retries at arrival, packed fp32 106; empty places 103-104.  Arrival as one addition
 // with release and acquire, where two fences stood around it: 7.2 us against 7.5 for the
 // one sequence, 79 against 81 for the two, 34.0 against 35.6 for two of 32768.
-#include <atomic>
-#include <chrono>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -914,19 +912,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int i = threadIdx.x; i < p.Hq * D / 8; i += kD8Threads)
                 reinterpret_cast<uint4 *>(p.o + static_cast<size_t>(z) * p.Hq * D)[i] =
                     make_uint4(0u, 0u, 0u, 0u);
-    }
-}
-
-// Per-call ids for the arrival words: 48 bits, never 0, different for every launch of the
-// process; the start is drawn from the clock, so that what another process or the
-// other decode left in a workspace is unlikely to match.
-static unsigned long long next_call_id() {
-    static std::atomic<unsigned long long> counter{
-        static_cast<unsigned long long>(
-            std::chrono::steady_clock::now().time_since_epoch().count()) * 0xD6E8FEB86659FD93ull};
-    for (;;) {
-        const unsigned long long id = counter.fetch_add(1) & 0xFFFFFFFFFFFFull;
-        if (id != 0) return id;
     }
 }
 

@@ -1,5 +1,7 @@
 // gqa_api.cu -- the extern "C" boundary: argument validation, error
 // reporting, device status, tensor-map encoding and dispatch to the kernels.
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -162,6 +164,16 @@ int encode_tmap_bf16_4d(CUtensorMap *map, const void *base, uint64_t n0, uint64_
                          (int)r, (unsigned long long)n0, (unsigned long long)n1,
                          (unsigned long long)n2, (unsigned long long)n3);
     return GQA_OK;
+}
+
+unsigned long long next_call_id() {
+    static std::atomic<unsigned long long> counter{
+        static_cast<unsigned long long>(
+            std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull};
+    for (;;) {
+        const unsigned long long id = counter.fetch_add(1) & 0xFFFFFFFFFFFFull;
+        if (id != 0) return id;
+    }
 }
 
 int encode_tmap_rows128(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows) {

@@ -82,6 +82,11 @@ int encode_tmap_bf16_4d(CUtensorMap *map, const void *base, uint64_t n0, uint64_
                         uint64_t n2, uint64_t n3, uint32_t b0, uint32_t b1, uint32_t b2,
                         uint32_t b3, int swizzle128, uint64_t n2_pitch = 0);
 
+// Id of one call for the arrival words of the two decodes: 48 bits, never 0, different for
+// every launch of the process, so that no other call's word in a shared workspace matches
+// (the start is drawn from the clock: another process' is unlikely to).
+unsigned long long next_call_id();
+
 // 2-D map over `rows` consecutive 128-byte rows, box of box_rows whole rows,
 // 128-byte swizzle.  Returns GQA_OK or GQA_ERR_CUDA.
 int encode_tmap_rows128(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
