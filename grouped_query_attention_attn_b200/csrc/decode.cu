@@ -203,7 +203,12 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int st = t % kDecStages;
         const uint32_t ph = (t / kDecStages) & 1;
         // warp-uniform outcome: ldmatrix and mma.sync below are warp-collective
-        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[st], ph, &abort_flag, status))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full_bar[st], ph, &abort_flag, status))) {
+            // the copies in flight land before the ring is reused and the block exits
+            for (int u = t; u < min(n_iter, t + kDecStages); ++u)
+                mbar_drain(&full_bar[u % kDecStages], (u / kDecStages) & 1, status);
+            break;
+        }
         uint8_t *kt = smem + st * Lay::kStageBytes;
         uint8_t *vt = kt + Lay::kTileBytes;
         // first key of this warp's slice, and how many keys of it are visible:
